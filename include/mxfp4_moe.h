@@ -63,12 +63,16 @@ enum {
 enum {
   MOE_DEV_OK = 0,
   MOE_DEV_BAD_EXPERT = 1,  /* moe_permute saw an expert id outside [0,E)   */
-  MOE_DEV_NO_MASS = 2,     /* block_accept_rejection: target row all zero  */
+  MOE_DEV_NO_MASS = 2,     /* block_accept_rejection: target row all zero;
+                              block_sample: no logit above -infinity       */
   MOE_DEV_BAD_TOKEN = 3,   /* a draft token outside [0,V)                   */
   MOE_DEV_TIMEOUT = 4,     /* a bounded device wait ran out                */
   MOE_DEV_BAD_INDEX = 5    /* checked build (MOE_CHECKS): a pair, row or
                               offset index outside its array, replaced by 0
-                              or (offsets) the call's experts left empty   */
+                              or (offsets) the call's experts left empty;
+                              every build: a page id outside the pool, or a
+                              position past a table, left out (block_kv_append,
+                              block_attention)                             */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -370,6 +374,112 @@ int block_accept_rejection_bonus(const float *p, const float *q, const int32_t *
  */
 int mxfp4_quantize(const uint16_t *w, int64_t R, int K, uint8_t *codes, uint8_t *scales,
                    moe_stream_t stream);
+
+/*
+ * block_kv_append -- a block's queries, keys and values from the packed
+ *   projection to where the attention reads them: RMS norm of every query
+ *   and key head, position rotation, and the append of keys and values to a
+ *   paged cache.  The pages name these ("RMSNorm, RoPE, KV-cache write")
+ *   among the steps that dominate a verify step at microsecond scale ([P3]);
+ *   they print no formula.  Reading taken here, the usual one, in one launch:
+ *     x^ = x / sqrt(mean_d x_d^2 + eps) * w     q and k heads, if norm != 0
+ *     (a, b) -> (a cos - b sin, a sin + b cos)  q and k, dims 0..rot-1
+ *   in float, rounded to bf16 once; v is copied bit for bit.
+ *   S sequences (slots) x N new tokens.  kv_len[s] is the cache length of
+ *   sequence s WITH its N new tokens, so token i has position
+ *   kv_len[s] - N + i.  A slot with kv_len <= 0 is not in use: its rows of
+ *   q_out and the cache are left as they were, and so are those of tokens
+ *   whose position would be negative (kv_len < N).  Position j of sequence s
+ *   lies in page block_table[s, j / page_size], row j % page_size.
+ *   qkv         [S, N, Hq + 2*Hkv, D] bf16: q heads, k heads, v heads
+ *   q_weight, k_weight [D] bf16 or NULL (ones); used if norm != 0
+ *   cos_sin     [max_pos, rot] float: row p holds the cosines of the rot/2
+ *               angles of position p, then their sines; NULL if rot == 0
+ *   rot         rotated dims per head, a multiple of 16, 0 <= rot <= D
+ *   interleaved 0: dim d turns with dim d + rot/2; 1: dim 2d with 2d+1
+ *   kv_len      [S] int32; block_table [S, max_pages] int32
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, updated
+ *   q_out       [S, N, Hq, D] bf16 out; must not overlap qkv
+ *   A page id outside [0, num_pages), a position past the table's row or past
+ *   max_pos sets MOE_DEV_BAD_INDEX and the token is left out.  Two tokens of
+ *   a call must not share a place in the cache (whichever lands last stays).
+ *   Limits: D 64, 128 or 256; Hq a multiple of Hkv, Hq <= 1024; 1 <= N <= 64;
+ *   S*N <= 2^20; max_pages*page_size < 2^31.  bf16 tensors and cos_sin 16-byte
+ *   aligned (else MOE_ERR_INVALID_ARG).
+ */
+int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, int norm,
+                    const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                    const float *cos_sin, int max_pos, int rot, int interleaved,
+                    const int32_t *kv_len, const int32_t *block_table, int max_pages,
+                    uint16_t *k_cache, uint16_t *v_cache, int num_pages, int page_size,
+                    uint16_t *q_out, moe_stream_t stream);
+
+/*
+ * block_attention -- attention of a block of N tokens per sequence over its
+ *   paged cache (N = 1: one new token).  The pages list the attention kernel
+ *   among a verify step's parts and a sliding window of 128 for the drafter
+ *   ([P1], [P3]), without formulas.  Reading taken here: the new tokens' keys
+ *   and values are in the cache already (block_kv_append); query head h reads
+ *   key/value head h / (Hq/Hkv); token i of sequence s, at position
+ *   p = kv_len[s] - N + i, sees the keys j with max(0, p - window + 1) <= j
+ *   <= p (window 0: all j <= p):
+ *     out = sum_j softmax_j(scale * q . k_j) v_j
+ *   with float statistics and sums; the softmax weights are rounded to bf16
+ *   for the product with v.  A token that sees no key (a slot with kv_len <=
+ *   0, or a negative position) gets zeros.  Cache rows at or past kv_len, and
+ *   pages that no token of the block sees, are never used, whatever they or
+ *   their page ids hold.  (Rows of the block's later tokens weigh 0 for its
+ *   earlier ones and, like every visible row, must be finite.)
+ *   q, out      [S, N, Hq, D] bf16
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16
+ *   block_table [S, max_pages] int32; kv_len [S] int32
+ *   workspace   device scratch of block_attention_workspace_bytes bytes,
+ *               256-byte aligned; its contents on entry do not matter
+ *   A page id outside [0, num_pages) sets MOE_DEV_BAD_INDEX and its keys are
+ *   left out; so does a kv_len past the table's row, whose slot counts as
+ *   empty.
+ *   Limits as block_kv_append; scale finite, window >= 0.
+ */
+size_t block_attention_workspace_bytes(int S, int N, int Hq, int Hkv, int D);
+
+int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
+                    const uint16_t *k_cache, const uint16_t *v_cache, int num_pages,
+                    int page_size, const int32_t *block_table, int max_pages,
+                    const int32_t *kv_len, float scale, int window, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * block_sample -- probabilities and tokens of S x K rows of logits under
+ *   temperature, top-k, top-p and min-p: the rows p and q that
+ *   block_accept_rejection reads, and the drafter's tokens.  (The pages verify
+ *   by rejection sampling, [P3] "数据流概览", and do not say how the
+ *   distributions are formed.)  For a row with logits l:
+ *     w_v = exp((l_v - max l) / temperature), W_v = floor(w_v * 2^40), double;
+ *     tokens ranked by logit, ties to the lowest index; kept is the longest
+ *     prefix of that ranking which every filter allows:
+ *       top-k  the first k;
+ *       top-p  the least prefix whose sum of W reaches ceil(top_p * sum of W
+ *              over the top-k prefix);
+ *       min-p  tokens with W_v >= floor(min_p * 2^40);
+ *     probs[v] = w_v / sum of kept w, 0 for the others, rounded once to float;
+ *     token = least kept v whose sum of kept W up to v exceeds
+ *             floor(sum of kept W * U / 2^24), U = u * 2^24.
+ *   The first-ranked token is always kept.  temperature <= 0 (or NaN): the
+ *   first-ranked token with probability 1.  top_k <= 0 or >= V, top_p >= 1 (or
+ *   NaN), min_p <= 0 (or NaN) switch a filter off; min_p > 1 counts as 1.
+ *   Logits of -infinity (masked tokens) have weight 0, NaN counts as
+ *   -infinity, +infinity takes all mass; a row with no logit above -infinity
+ *   sets MOE_DEV_NO_MASS: token -1, probs 0.
+ *   logits [S, K, V] float; temperature, top_p, min_p [S] float, top_k [S]
+ *   int32 (a sequence's setting holds for its K rows), each NULL for off;
+ *   u [S, K] float uniforms in [0,1), multiples of 2^-24; token [S, K] int32
+ *   out (u and token both given or both NULL); probs [S, K, V] float out or
+ *   NULL, must not overlap logits.
+ *   Limits: K >= 1, 1 <= V <= 2^20, S*K <= 2^20.
+ */
+int block_sample(const float *logits, int S, int K, int V, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                 int32_t *token, float *probs, moe_stream_t stream);
 
 /*
  * moe_get_device_status -- synchronise `stream`, then report the sticky

@@ -53,6 +53,13 @@ SIGNATURES = {
     "block_accept_rejection_bonus": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                               _vp, _vp, _vp]),
     "mxfp4_quantize": (_c_int, [_vp, ctypes.c_int64, _c_int, _vp, _vp, _vp]),
+    "block_kv_append": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
+                                 _c_float, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp,
+                                 _c_int, _c_int, _vp, _vp]),
+    "block_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "block_attention": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_int,
+                                 _c_int, _vp, _c_int, _vp, _c_float, _c_int, _vp, _vp, _c_size, _vp]),
+    "block_sample": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_get_device_status": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     "moe_clear_device_status": (_c_int, [_vp]),
     "moe_set_wait_limit_ns": (_c_int, [ctypes.c_uint64, _vp]),
@@ -315,6 +322,139 @@ def mxfp4_quantize(w, codes=None, scales=None, stream=None):
     _check(lib().mxfp4_quantize(_ptr(w, torch.bfloat16, "w"), R, K, _ptr(codes, torch.uint8),
                                 _ptr(scales, torch.uint8), _stream(stream)), "mxfp4_quantize")
     return codes, scales
+
+
+class _On:
+    """The device and stream of a call: every tensor given lies on one CUDA
+    device, which is current inside the context; outputs and scratch allocated
+    there belong to the stream the kernels run on."""
+
+    def __init__(self, stream, **tensors):
+        devs = {t.device for t in tensors.values() if t is not None}
+        bad = [n for n, t in tensors.items() if t is not None and not t.is_cuda]
+        if bad:
+            raise ValueError(f"{bad[0]} must be a CUDA tensor")
+        if len(devs) != 1:
+            raise ValueError("tensors on different devices: "
+                             + ", ".join(f"{n} {t.device}" for n, t in tensors.items() if t is not None))
+        self.device = devs.pop()
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if self.stream.device != self.device:
+            raise ValueError(f"stream of {self.stream.device} for tensors on {self.device}")
+        self._ctx = torch.cuda.stream(self.stream)     # also makes its device current
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _cache_shapes(k_cache, v_cache, kv_len, block_table, S):
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, D], block_table [S, max_pages]")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(kv_len, (S,), "kv_len")
+    _shape(block_table, (S, block_table.shape[1]), "block_table")
+    return tuple(k_cache.shape) + (block_table.shape[1],)
+
+
+def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_weight=None,
+                    k_weight=None, norm=True, eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """Head norms of q and k, rotation, append of k and v to the paged cache.
+
+    qkv [S, N, Hq + 2*Hkv, D] bf16; kv_len [S] int32 with the N new tokens counted;
+    block_table [S, max_pages] int32; caches [pages, Hkv, page_size, D] bf16, updated in
+    place; cos_sin [max_pos, rot] float or None (no rotation).  Returns q [S, N, Hq, D];
+    rows of slots not in use are zero where the call allocates q, else left as they were."""
+    with _On(stream, qkv=qkv, kv_len=kv_len, block_table=block_table, k_cache=k_cache,
+             v_cache=v_cache, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, q_out=q_out) as on:
+        S, N, heads, D = qkv.shape
+        pages, Hkv, page_size, _, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
+        _shape(k_cache, (pages, Hkv, page_size, D), "k_cache")
+        Hq = heads - 2 * Hkv
+        if q_out is None and Hq > 0:
+            q_out = torch.zeros((S, N, Hq, D), dtype=torch.bfloat16, device=on.device)
+        _shape(q_out, (S, N, Hq, D), "q_out")
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            _shape(w, (D,), name)
+        max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+        _check(lib().block_kv_append(
+            _ptr(qkv, torch.bfloat16, "qkv"), S, N, Hq, Hkv, D, int(norm),
+            _ptr(q_weight, torch.bfloat16, "q_weight"), _ptr(k_weight, torch.bfloat16, "k_weight"),
+            float(eps), _ptr(cos_sin, torch.float32, "cos_sin"), max_pos, rot, int(interleaved),
+            _ptr(kv_len, torch.int32, "kv_len"), _ptr(block_table, torch.int32, "block_table"),
+            max_pages, _ptr(k_cache, torch.bfloat16, "k_cache"),
+            _ptr(v_cache, torch.bfloat16, "v_cache"), pages, page_size,
+            _ptr(q_out, torch.bfloat16, "q_out"), _stream(on.stream)), "block_kv_append")
+    return q_out
+
+
+def block_attention_workspace_bytes(S, N, Hq, Hkv, D):
+    return int(lib().block_attention_workspace_bytes(S, N, Hq, Hkv, D))
+
+
+def alloc_attention_workspace(S, N, Hq, Hkv, D, device):
+    return torch.empty(max(block_attention_workspace_bytes(S, N, Hq, Hkv, D), 1),
+                       dtype=torch.uint8, device=device)
+
+
+def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window=0, out=None,
+                    workspace=None, stream=None):
+    """Attention of N tokens per sequence over the paged cache; q [S, N, Hq, D] bf16.
+
+    scale defaults to D ** -0.5; window 0 sees the whole cache.  Returns out [S, N, Hq, D]."""
+    with _On(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_len=kv_len,
+             out=out, workspace=workspace) as on:
+        S, N, Hq, D = q.shape
+        pages, Hkv, page_size, _, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
+        _shape(k_cache, (pages, Hkv, page_size, D), "k_cache")
+        if out is None:
+            out = torch.empty_like(q)
+        _shape(out, q.shape, "out")
+        if workspace is None:
+            workspace = alloc_attention_workspace(S, N, Hq, Hkv, D, on.device)
+        _check(lib().block_attention(
+            _ptr(q, torch.bfloat16, "q"), S, N, Hq, Hkv, D, _ptr(k_cache, torch.bfloat16, "k_cache"),
+            _ptr(v_cache, torch.bfloat16, "v_cache"), pages, page_size,
+            _ptr(block_table, torch.int32, "block_table"), max_pages,
+            _ptr(kv_len, torch.int32, "kv_len"), float(D ** -0.5 if scale is None else scale),
+            int(window), _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace"),
+            workspace.numel(), _stream(on.stream)), "block_attention")
+    return out
+
+
+def block_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None,
+                 with_probs=False, token=None, probs=None, stream=None):
+    """logits [S, K, V] -> (token [S, K] int32 or None, probs [S, K, V] float or None).
+
+    Tokens are drawn where u [S, K] is given; probabilities are written where
+    with_probs is set or probs given.  The filters are [S] tensors or None (off)."""
+    with _On(stream, logits=logits, u=u, temperature=temperature, top_k=top_k, top_p=top_p,
+             min_p=min_p, token=token, probs=probs) as on:
+        S, K, V = logits.shape
+        _shape(u, (S, K), "u")
+        for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+            _shape(t, (S,), name)
+        if u is not None and token is None:
+            token = torch.empty((S, K), dtype=torch.int32, device=on.device)
+        if with_probs and probs is None:
+            probs = torch.empty((S, K, V), dtype=torch.float32, device=on.device)
+        _shape(token, (S, K), "token")
+        _shape(probs, (S, K, V), "probs")
+        f32 = torch.float32
+        _check(lib().block_sample(
+            _ptr(logits, f32, "logits"), S, K, V, _ptr(temperature, f32, "temperature"),
+            _ptr(top_k, torch.int32, "top_k"), _ptr(top_p, f32, "top_p"), _ptr(min_p, f32, "min_p"),
+            _ptr(u, f32, "u"), _ptr(token, torch.int32, "token"), _ptr(probs, f32, "probs"),
+            _stream(on.stream)), "block_sample")
+    return token, probs
 
 
 def moe_get_device_status(stream=None):

@@ -58,6 +58,8 @@ __device__ __forceinline__ bool offsets_ok(const int32_t *off, int E, long P) {
 
 constexpr unsigned FULL = 0xffffffffu;
 
+constexpr int BLOCK_MAX_TOKENS = 64;   // tokens per sequence of a drafted block
+
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialisation, so the next kernel on the stream
 // may become resident (and run its prologue) while this one finishes.

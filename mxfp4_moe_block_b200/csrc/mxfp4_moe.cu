@@ -1,6 +1,7 @@
 // mxfp4_moe.cu -- the C ABI of include/mxfp4_moe.h: argument checks, kernel
 // choice and launches.  Every kernel of the library is compiled into this one
 // translation unit (the .cuh files), for sm_100a.
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
@@ -15,6 +16,9 @@
 #include "combine.cuh"
 #include "accept.cuh"
 #include "quantize.cuh"
+#include "kv_append.cuh"
+#include "attention.cuh"
+#include "sample.cuh"
 
 using namespace moe;
 
@@ -462,6 +466,89 @@ int mxfp4_quantize(const uint16_t *w, int64_t R, int K, uint8_t *codes, uint8_t 
   const unsigned grid = (unsigned)std::min<size_t>(blocks, (size_t)dev->sms * 8);
   return launched(launch_pdl(mxfp4_quantize_kernel, grid, QUANT_THREADS, 0, (cudaStream_t)stream,
                              w, n8, codes, scales));
+}
+
+// ------------------------------------------------ append to the cache --
+static int heads_check(int S, int N, int Hq, int Hkv, int D) {
+  if (S < 0 || N < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || D < 1) return MOE_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return MOE_ERR_UNSUPPORTED;
+  if (N > BLOCK_MAX_TOKENS || Hq > 1024 || (long long)S * N > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static bool misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, int norm,
+                    const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                    const float *cos_sin, int max_pos, int rot, int interleaved,
+                    const int32_t *kv_len, const int32_t *block_table, int max_pages,
+                    uint16_t *k_cache, uint16_t *v_cache, int num_pages, int page_size,
+                    uint16_t *q_out, moe_stream_t stream) {
+  const CallRange range("block_kv_append");
+  const int st = heads_check(S, N, Hq, Hkv, D);
+  if (st != MOE_OK) return st;
+  if (rot < 0 || rot > D || rot % 16 || (rot && (!cos_sin || max_pos < 1)) || max_pages < 1 ||
+      num_pages < 1 || page_size < 1 || (norm && !(eps >= 0.f)))
+    return MOE_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (S == 0) return MOE_OK;
+  if (!qkv || !kv_len || !block_table || !k_cache || !v_cache || !q_out) return MOE_ERR_INVALID_ARG;
+  if (misaligned16(qkv) || misaligned16(q_weight) || misaligned16(k_weight) ||
+      misaligned16(cos_sin) || misaligned16(k_cache) || misaligned16(v_cache) ||
+      misaligned16(q_out))
+    return MOE_ERR_INVALID_ARG;
+  const AppendArgs a{qkv, N, Hq, Hkv, norm ? 1 : 0, q_weight, k_weight, eps, cos_sin, max_pos, rot,
+                     interleaved ? 1 : 0, kv_len, block_table, max_pages, num_pages, page_size,
+                     k_cache, v_cache, q_out};
+  return launched(launch_append<1>(a, S * N, D, (cudaStream_t)stream));
+}
+
+// -------------------------------------------------------------- attention --
+size_t block_attention_workspace_bytes(int S, int N, int Hq, int Hkv, int D) {
+  if (heads_check(S, N, Hq, Hkv, D) != MOE_OK) return 0;
+  return 256;
+}
+
+int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
+                    const uint16_t *k_cache, const uint16_t *v_cache, int num_pages,
+                    int page_size, const int32_t *block_table, int max_pages,
+                    const int32_t *kv_len, float scale, int window, uint16_t *out,
+                    void *workspace, size_t workspace_bytes, moe_stream_t stream) {
+  const CallRange range("block_attention");
+  const int st = heads_check(S, N, Hq, Hkv, D);
+  if (st != MOE_OK) return st;
+  if (max_pages < 1 || num_pages < 1 || page_size < 1 || window < 0 || !(fabsf(scale) < INFINITY))
+    return MOE_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (S == 0) return MOE_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !kv_len || !out || !workspace)
+    return MOE_ERR_INVALID_ARG;
+  if (misaligned16(q) || misaligned16(k_cache) || misaligned16(v_cache) || misaligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < block_attention_workspace_bytes(S, N, Hq, Hkv, D) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return MOE_ERR_WORKSPACE;
+  const AttnArgs a{q, S, N, Hq, Hkv, k_cache, v_cache, num_pages, page_size, block_table, max_pages,
+                   kv_len, scale, window, out};
+  const long rows = (long)S * N * Hq;
+  auto kern = D == 64 ? attn_rows_kernel<64> : D == 128 ? attn_rows_kernel<128> : attn_rows_kernel<256>;
+  return launched(launch_pdl(kern, (unsigned)((rows + ATTN_ROW_WARPS - 1) / ATTN_ROW_WARPS),
+                             32 * ATTN_ROW_WARPS, 0, (cudaStream_t)stream, a));
+}
+
+// --------------------------------------------------------------- sampling --
+int block_sample(const float *logits, int S, int K, int V, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                 int32_t *token, float *probs, moe_stream_t stream) {
+  const CallRange range("block_sample");
+  if (S < 0 || K < 1 || V < 1) return MOE_ERR_INVALID_ARG;
+  if (V > SAMPLE_MAX_V || (long long)S * K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if ((token != nullptr) != (u != nullptr) || (!token && !probs)) return MOE_ERR_INVALID_ARG;
+  if (S == 0) return MOE_OK;
+  if (!logits) return MOE_ERR_INVALID_ARG;
+  const SampleArgs a{logits, K, V, temperature, top_k, top_p, min_p, u, token, probs};
+  return launched(launch_pdl(sample_kernel, (unsigned)(S * K), SAMPLE_THREADS, 0,
+                             (cudaStream_t)stream, a));
 }
 
 // ----------------------------------------------------------------- status --
