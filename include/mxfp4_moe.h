@@ -438,7 +438,8 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
  *   A page id outside [0, num_pages) sets MOE_DEV_BAD_INDEX and its keys are
  *   left out; so does a kv_len past the table's row, whose slot counts as
  *   empty.
- *   Limits as block_kv_append; scale finite, window >= 0.
+ *   Limits as block_kv_append; scale finite and >= 0, window >= 0.  Two kernels
+ *   run: the attention, then the join of sequences that were cut.
  */
 size_t block_attention_workspace_bytes(int S, int N, int Hq, int Hkv, int D);
 

@@ -1,6 +1,7 @@
 // mxfp4_moe.cu -- the C ABI of include/mxfp4_moe.h: argument checks, kernel
 // choice and launches.  Every kernel of the library is compiled into this one
 // translation unit (the .cuh files), for sm_100a.
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -506,7 +507,7 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
 // -------------------------------------------------------------- attention --
 size_t block_attention_workspace_bytes(int S, int N, int Hq, int Hkv, int D) {
   if (heads_check(S, N, Hq, Hkv, D) != MOE_OK) return 0;
-  return 256;
+  return attn_ws(N, Hq, Hkv, D).total;
 }
 
 int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
@@ -517,7 +518,7 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
   const CallRange range("block_attention");
   const int st = heads_check(S, N, Hq, Hkv, D);
   if (st != MOE_OK) return st;
-  if (max_pages < 1 || num_pages < 1 || page_size < 1 || window < 0 || !(fabsf(scale) < INFINITY))
+  if (max_pages < 1 || num_pages < 1 || page_size < 1 || window < 0 || !(scale >= 0.f && scale < INFINITY))
     return MOE_ERR_INVALID_ARG;
   if ((long long)max_pages * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (S == 0) return MOE_OK;
@@ -528,12 +529,25 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
   if (workspace_bytes < block_attention_workspace_bytes(S, N, Hq, Hkv, D) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255))
     return MOE_ERR_WORKSPACE;
-  const AttnArgs a{q, S, N, Hq, Hkv, k_cache, v_cache, num_pages, page_size, block_table, max_pages,
-                   kv_len, scale, window, out};
-  const long rows = (long)S * N * Hq;
-  auto kern = D == 64 ? attn_rows_kernel<64> : D == 128 ? attn_rows_kernel<128> : attn_rows_kernel<256>;
-  return launched(launch_pdl(kern, (unsigned)((rows + ATTN_ROW_WARPS - 1) / ATTN_ROW_WARPS),
-                             32 * ATTN_ROW_WARPS, 0, (cudaStream_t)stream, a));
+  const DeviceInfo *dev = device_info();
+  if (!dev) return MOE_ERR_CUDA;
+  // (a scale of 0 weighs every visible key alike; as the smallest float it
+  // still keeps the -infinity of masked keys)
+  AttnArgs a{};
+  a.q = q;
+  a.S = S, a.N = N, a.Hq = Hq, a.Hkv = Hkv;
+  a.k_cache = k_cache, a.v_cache = v_cache;
+  a.num_pages = num_pages, a.page_size = page_size;
+  a.block_table = block_table, a.max_pages = max_pages;
+  a.kv_len = kv_len;
+  a.scale_log2 = fmaxf(scale * 1.44269504f, FLT_MIN);
+  a.window = window;
+  a.out = out;
+  uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  return D == 64    ? attn_launch<64>(a, ws, dev->sms, cs)
+         : D == 128 ? attn_launch<128>(a, ws, dev->sms, cs)
+                    : attn_launch<256>(a, ws, dev->sms, cs);
 }
 
 // --------------------------------------------------------------- sampling --

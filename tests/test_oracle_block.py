@@ -158,7 +158,7 @@ def test_append_refusals(library, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), 1), (dict(N=0), 1), (dict(N=65), 2), (dict(Hq=7), 1), (dict(D=80), 2),
     (dict(pages=0), 1), (dict(ps=0), 1), (dict(max_pages=0), 1), (dict(window=-1), 1),
-    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
     (dict(max_pages=1 << 20, ps=1 << 12), 2), (dict(q=None), 1), (dict(k=None), 1),
     (dict(v=None), 1), (dict(table=None), 1), (dict(kv_len=None), 1), (dict(out=None), 1),
     (dict(ws=None), 1), (dict(ws_bytes=16), 4), (dict(ws=A + 16), 4), (dict(q=A + 2), 1),
