@@ -462,7 +462,8 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
  *       top-p  the least prefix whose sum of W reaches ceil(top_p * sum of W
  *              over the top-k prefix);
  *       min-p  tokens with W_v >= floor(min_p * 2^40);
- *     probs[v] = w_v / sum of kept w, 0 for the others, rounded once to float;
+ *     probs[v] = w_v / sum of kept w, 0 for the others, as float (weight,
+ *                reciprocal and product rounded: within 2^-22 of the value);
  *     token = least kept v whose sum of kept W up to v exceeds
  *             floor(sum of kept W * U / 2^24), U = u * 2^24.
  *   The first-ranked token is always kept.  temperature <= 0 (or NaN): the
@@ -476,7 +477,7 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
  *   u [S, K] float uniforms in [0,1), multiples of 2^-24; token [S, K] int32
  *   out (u and token both given or both NULL); probs [S, K, V] float out or
  *   NULL, must not overlap logits.
- *   Limits: K >= 1, 1 <= V <= 2^20, S*K <= 2^20.
+ *   Limits: 1 <= K <= 64, 1 <= V <= 393216, S*K <= 2^20.
  */
 int block_sample(const float *logits, int S, int K, int V, const float *temperature,
                  const int32_t *top_k, const float *top_p, const float *min_p, const float *u,

@@ -40,6 +40,7 @@ struct DeviceInfo {
   bool ready = false;
   int sms = 0;
   bool greedy_attr = false;   // non-portable cluster size allowed for greedy_kernel
+  bool sample_attr = false;   // dynamic shared memory of sample_kernel
   bool permute_attr = false;  // 33*1024 ints of dynamic shared memory for the permutation
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -556,13 +557,43 @@ int block_sample(const float *logits, int S, int K, int V, const float *temperat
                  int32_t *token, float *probs, moe_stream_t stream) {
   const CallRange range("block_sample");
   if (S < 0 || K < 1 || V < 1) return MOE_ERR_INVALID_ARG;
-  if (V > SAMPLE_MAX_V || (long long)S * K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (V > SAMPLE_MAX_V || K > BLOCK_MAX_TOKENS || (long long)S * K > (1 << 20))
+    return MOE_ERR_UNSUPPORTED;
   if ((token != nullptr) != (u != nullptr) || (!token && !probs)) return MOE_ERR_INVALID_ARG;
   if (S == 0) return MOE_OK;
   if (!logits) return MOE_ERR_INVALID_ARG;
-  const SampleArgs a{logits, K, V, temperature, top_k, top_p, min_p, u, token, probs};
-  return launched(launch_pdl(sample_kernel, (unsigned)(S * K), SAMPLE_THREADS, 0,
-                             (cudaStream_t)stream, a));
+  DeviceInfo *dev = const_cast<DeviceInfo *>(device_info());
+  if (!dev) return MOE_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (!dev->sample_attr) {
+      const int most = (int)sample_smem_bytes(sample_slice(SAMPLE_MAX_V, SAMPLE_MAX_CLUSTER), true);
+      if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
+          cudaSuccess)
+        return launch_status();
+      dev->sample_attr = true;
+    }
+  }
+  const int rows = S * K, c = sample_cluster(rows, V, dev->sms), slice = sample_slice(V, c);
+  const SampleArgs a{logits, K, V, temperature, top_k, top_p, min_p, u, token, probs, slice};
+  // (rows along y: a grid's x is its clusters' width; 65535 rows to a launch)
+  for (int r0 = 0; r0 < rows; r0 += 65535 / K * K) {
+    SampleArgs part = a;
+    const int n = std::min(rows - r0, 65535 / K * K);
+    const size_t at = (size_t)r0 * V;
+    part.logits += at;
+    if (probs) part.probs += at;
+    if (token) part.token += r0, part.u += r0;
+    if (temperature) part.temperature += r0 / K;
+    if (top_k) part.top_k += r0 / K;
+    if (top_p) part.top_p += r0 / K;
+    if (min_p) part.min_p += r0 / K;
+    const int st = launched(launch_pdl_cluster(
+        sample_kernel, dim3((unsigned)c, (unsigned)n), SAMPLE_THREADS,
+        sample_smem_bytes(slice, top_k || top_p), (unsigned)c, (cudaStream_t)stream, part));
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
 }
 
 // ----------------------------------------------------------------- status --

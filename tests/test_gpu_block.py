@@ -13,8 +13,9 @@ step, 2^-24):
   the weight's rounding to bf16 adds HALF; numerator and sum carry these, so
   the result is off by (HALF + 4 dz + 2^-17) of the weighted mean of |v|, and by
   HALF of itself for the last rounding.
-* sampling: tokens equal; a probability is the quotient of a weight and a sum,
-  each within 2^-23, rounded once: 2^-22 relative, or one float denormal.
+* sampling: tokens equal; a probability is a weight times the reciprocal of a
+  sum (both within 2^-44 as doubles), three roundings to float: 3 EPS < 2^-22
+  relative, or one float denormal.
 """
 import math
 

@@ -174,8 +174,8 @@ def test_attention_workspace_query(library):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(S=-1), 1), (dict(K=0), 1), (dict(V=0), 1), (dict(V=(1 << 20) + 1), 2),
-    (dict(S=1 << 11, K=1 << 10), 2), (dict(u=None), 1), (dict(token=None), 1),
+    (dict(S=-1), 1), (dict(K=0), 1), (dict(V=0), 1), (dict(V=393217), 2), (dict(K=65), 2),
+    (dict(S=1 << 15, K=64), 2), (dict(u=None), 1), (dict(token=None), 1),
     (dict(u=None, token=None), 1), (dict(logits=None), 1), (dict(S=0, logits=None), 0)])
 def test_sample_refusals(library, kw, status):
     assert sample(library, **kw) == status
