@@ -21,13 +21,15 @@
 // again by the bits of the logit, three times at most, and a group of equal
 // logits is cut by a quotient and a count.
 //
-// The exponentials are the arithmetic: a double costs an SM 1/64 cycle an
-// operation and one weight takes 14, ~4.5 weights per cycle and SM, against ~10
-// logits per cycle that HBM delivers to an SM.  So each kept token's weight is
+// The exponentials are the arithmetic: an SM does 64 double operations a cycle
+// and a weight with its mass takes 13, ~5 weights per cycle and SM, against ~6
+// logits per cycle that HBM delivers to an SM (and as many probabilities taken
+// back).  So each kept token's weight is
 // computed once (twice for top-p over a whole row), the float of it stays in
 // shared memory for the probabilities, and the draw recomputes 1/16 of one
 // slice.
 #pragma once
+#include <cfloat>
 #include <cooperative_groups.h>
 #include "common.cuh"
 
@@ -38,7 +40,8 @@ constexpr int SAMPLE_THREADS = 512;
 constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
 constexpr int SAMPLE_MAX_V = 393216;
 constexpr int SAMPLE_BUCKETS = 1024;     // two per thread
-constexpr int SAMPLE_LIST = 1024;        // tokens the first CTA sorts
+constexpr int SAMPLE_LIST = 1024;        // tokens the first CTA sorts, two per thread
+constexpr int SAMPLE_SMALL_K = 256;      // top-k found from the threads' own maxima
 constexpr int SAMPLE_MAX_CLUSTER = 8;
 constexpr unsigned long long SAMPLE_ONE = 1ull << 40;
 
@@ -54,9 +57,9 @@ struct SampleArgs {
   int slice;                     // tokens of a CTA, a multiple of 4
 };
 
-// In shared memory a logit is canonical: NaN becomes -infinity, -0 becomes 0,
-// and places outside the row hold NaN.
-__device__ __forceinline__ float canonical(float x) { return x == x ? x + 0.f : -INFINITY; }
+// In shared memory a logit is canonical: -0 becomes 0; NaN, which also fills
+// the places outside the row, stays and counts as no token at all.
+__device__ __forceinline__ float canonical(float x) { return x + 0.f; }
 
 // order-preserving key of a canonical logit
 __device__ __forceinline__ uint32_t logit_key(float x) {
@@ -67,33 +70,39 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// w = 2^((x - top) c), c = log2(e) / temperature.  The exponent's integer part
-// is split off by adding 1.5 2^52; 2^f on [-1/2, 1/2] is 1 + f p(f), p of degree
-// 8 fitted to the least relative error at Chebyshev nodes: 2^-45.7.  Weights
-// below 2^-1000 count as 0.
-__device__ __forceinline__ double sample_weight(float x, float top, double c) {
-  if (x == top) return 1.0;
-  const double t = ((double)x - (double)top) * c;
-  if (!(t > -1000.0)) return 0.0;
-  const double shifted = t + 6755399441055744.0;
-  const double f = t - (shifted - 6755399441055744.0);
-  double p = 1.013516777919082e-07;
-  p = fma(p, f, 1.3258416121625738e-06);
-  p = fma(p, f, 1.525306990799785e-05);
-  p = fma(p, f, 0.00015403440465134365);
-  p = fma(p, f, 0.0013333557458737857);
-  p = fma(p, f, 0.009618129181844376);
-  p = fma(p, f, 0.05550410866978266);
-  p = fma(p, f, 0.2402265069571947);
-  p = fma(p, f, 0.6931471805598506);
-  p = fma(p, f, 1.0);
-  const long long bits = __double_as_longlong(p) +
-                         ((long long)(int)(uint32_t)__double_as_longlong(shifted) << 52);
-  return __longlong_as_double(bits);
-}
-// floor(w 2^40), w <= 1: added to 2^52 the integer part is the low bits
+// w = 2^(d c), d = x - top <= 0, c = log2(e) / temperature, for d c > -1000 (the
+// caller takes 0 for less).  The exponent's nearest integer comes from float (it
+// need not be exact: the remainder f is), 2^f on [-1/2, 1/2] is 1 + f p(f), p of
+// degree 7 fitted to the least relative error at Chebyshev nodes: 2^-40, the
+// masses' own step.  11 double operations and two conversions.  (Temperatures
+// below 1e-36 count as 1e-36, so that the scale stays finite in float.)
+struct SampleScale {
+  double top, c;
+  float ftop, fc, below;          // weights of x - top <= below are 0
+  __device__ __forceinline__ SampleScale(float t, double scale)
+      : top((double)t), c(fmin(scale, 1e36)), ftop(t), fc((float)c),
+        below(fmaxf((float)(-1000.0 / c), -FLT_MAX)) {}
+  __device__ __forceinline__ bool positive(float x) const { return x - ftop > below; }   // NaN: no
+  __device__ __forceinline__ double weight(float x) const {
+    const float magic = 12582912.f;                                 // 1.5 2^23
+    const float shifted = fmaf(x - ftop, fc, magic);
+    const double f = fma((double)x - top, c, -(double)(shifted - magic));
+    double p = 1.318882399508972e-06;
+    p = fma(p, f, 1.5309693155944608e-05);
+    p = fma(p, f, 0.00015403775196491106);
+    p = fma(p, f, 0.001333345225539645);
+    p = fma(p, f, 0.00961812869532959);
+    p = fma(p, f, 0.05550410939101241);
+    p = fma(p, f, 0.2402265069773642);
+    p = fma(p, f, 0.6931471805465889);
+    p = fma(p, f, 1.0);
+    return __hiloint2double(__double2hiint(p) + (__float_as_int(shifted) << 20), __double2loint(p));
+  }
+};
+// floor(w 2^40), 2^-1000 < w <= 1: added to 2^52 the integer part is the low bits
 __device__ __forceinline__ unsigned long long sample_mass(double w) {
-  return (unsigned long long)__double_as_longlong(__dadd_rd(w * 1099511627776.0, 4503599627370496.0)) &
+  const double scaled = __hiloint2double(__double2hiint(w) + (40 << 20), __double2loint(w));
+  return (unsigned long long)__double_as_longlong(__dadd_rd(scaled, 4503599627370496.0)) &
          0xfffffffffffffull;
 }
 
@@ -107,6 +116,7 @@ struct SampleRow {
     u64 bar;                   // top-p's mass
     uint32_t thr;
     int cut;
+    float inv;                 // 1 / sum of the kept weights, where the list settles a row
   };
   struct Shared {
     u64 xch[8][SAMPLE_MAX_CLUSTER];
@@ -209,47 +219,49 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     return m;
   };
 
-  // ---- the slice into shared memory; the largest logit and its first index ----
-  u64 best = 0;                                                     // key << 32 | ~index
+  // ---- the slice into shared memory; the largest logit ----
+  float most = -INFINITY;
   {
     constexpr int U = 4;
+    const float none = __int_as_float(0x7fffffff);
     for (int j = tid; j < units; j += U * SAMPLE_THREADS) {
       float4 q[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int unit = j + i * SAMPLE_THREADS, v = v0 + 4 * unit;
-        const float none = __int_as_float(0x7fffffff);
         if (unit >= units) break;
         if (v >= c0 && v + 3 < c1) {
           q[i] = __ldcs(reinterpret_cast<const float4 *>(x + v));
-          q[i] = make_float4(canonical(q[i].x), canonical(q[i].y), canonical(q[i].z), canonical(q[i].w));
         } else {
-          q[i].x = v >= c0 && v < c1 ? canonical(x[v]) : none;
-          q[i].y = v + 1 >= c0 && v + 1 < c1 ? canonical(x[v + 1]) : none;
-          q[i].z = v + 2 >= c0 && v + 2 < c1 ? canonical(x[v + 2]) : none;
-          q[i].w = v + 3 >= c0 && v + 3 < c1 ? canonical(x[v + 3]) : none;
+          q[i].x = v >= c0 && v < c1 ? x[v] : none;
+          q[i].y = v + 1 >= c0 && v + 1 < c1 ? x[v + 1] : none;
+          q[i].z = v + 2 >= c0 && v + 2 < c1 ? x[v + 2] : none;
+          q[i].w = v + 3 >= c0 && v + 3 < c1 ? x[v + 3] : none;
         }
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int unit = j + i * SAMPLE_THREADS, v = v0 + 4 * unit;
+        const int unit = j + i * SAMPLE_THREADS;
         if (unit >= units) break;
+        q[i] = make_float4(canonical(q[i].x), canonical(q[i].y), canonical(q[i].z), canonical(q[i].w));
         val4[unit] = q[i];
-        const float e[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (e[k] == e[k]) {
-            const u64 cand = ((u64)logit_key(e[k]) << 32) | (uint32_t)~(uint32_t)(v + k);
-            best = cand > best ? cand : best;
-          }
+        most = fmaxf(most, fmaxf(fmaxf(q[i].x, q[i].y), fmaxf(q[i].z, q[i].w)));   // (skips NaN)
       }
     }
   }
   cluster.barrier_wait();
-  best = cluster_max(best);
-  const uint32_t top_key = (uint32_t)(best >> 32);
-  const int top_token = (int)~(uint32_t)best;
-  const float top = key_logit(top_key);
+  float top = key_logit((uint32_t)cluster_max(logit_key(most)));
+  // +infinity takes all mass: such a row counts as 0 there and -infinity elsewhere
+  const bool inf_row = top == INFINITY;
+  auto infinite = [&](float l) { return inf_row ? (l == INFINITY ? 0.f : l == l ? -INFINITY : l) : l; };
+  if (inf_row) {
+    for (int j = tid; j < units; j += SAMPLE_THREADS) {
+      const float4 q = val4[j];
+      val4[j] = make_float4(infinite(q.x), infinite(q.y), infinite(q.z), infinite(q.w));
+    }
+    top = 0.f;
+    __syncthreads();
+  }
 
   // probabilities: 16-byte stores where the output's units are the input's
   float *const probs = a.probs ? a.probs + (size_t)row * V : nullptr;
@@ -271,6 +283,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const double T = a.temperature ? (double)__ldg(a.temperature + s) : 1.0;
   const bool none = top == -INFINITY;
   if (none || !(T > 0.0)) {                       // no mass, or the first-ranked token alone
+    uint32_t first = 0;                           // ~index of the first largest logit
+    if (!none) {
+      for (int j = tid; j < units; j += SAMPLE_THREADS) {
+        const float4 q = val4[j];
+        const int i = q.x == top ? 0 : q.y == top ? 1 : q.z == top ? 2 : q.w == top ? 3 : 4;
+        if (i < 4) {
+          first = ~(uint32_t)(v0 + 4 * j + i);
+          break;
+        }
+      }
+      first = (uint32_t)cluster_max(first);
+    }
+    const int top_token = (int)~first;
     if (rank == 0 && tid == 0) {
       if (none) raise_status(MOE_DEV_NO_MASS);
       if (a.token) a.token[row] = none ? -1 : top_token;
@@ -282,8 +307,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       });
     return;                                       // (no remote access after the exchange)
   }
-  const double c = 1.4426950408889634 / T;
-  auto weight = [&](float l) { return sample_weight(l, top, c); };
+  const SampleScale z(top, 1.4426950408889634 / T);
+  auto mass_at = [&](float l) -> u64 { return z.positive(l) ? sample_mass(z.weight(l)) : 0; };
 
   // ---- the threshold: kept are keys above thr, and at thr the tokens <= cut ----
   uint32_t thr = 0;
@@ -299,7 +324,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     u64 *const lead_list = cluster.map_shared_rank(list, 0);
     int *const lead_n = cluster.map_shared_rank(&sh.list_n, 0);
 
-    // every token of the slice that is still kept, with its key
+    // every token of the slice that is still kept
     auto for_kept = [&](auto f) {
       for (int j = tid; j < units; j += SAMPLE_THREADS) {
         const float4 q = val4[j];
@@ -307,27 +332,88 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (!(e[i] == e[i])) continue;
-          const uint32_t key = logit_key(e[i]);
           const int v = v0 + 4 * j + i;
-          if (key > thr || (key == thr && v <= cut)) f(e[i], key, v);
+          if (thr) {
+            const uint32_t key = logit_key(e[i]);
+            if (key < thr || (key == thr && v > cut)) continue;
+          }
+          f(e[i], v);
         }
       }
     };
-    // tokens to the first CTA's list
-    auto push = [&](bool take, uint32_t key, int v) {
-      if (take) {
-        const int at = atomicAdd(lead_n, 1);
-        if (at < SAMPLE_LIST) lead_list[at] = ((u64)key << 32) | (uint32_t)~(uint32_t)v;
-      }
+    auto clear = [&]() {
+      for (int i = tid; i < SAMPLE_BUCKETS; i += SAMPLE_THREADS) h_cnt[i] = h_lo[i] = h_hi[i] = 0;
+      if (tid == 0) sh.list_n = 0;
+      __syncthreads();
     };
-    // the list, sorted by key and index (descending words), padded with zeros;
-    // returns its length
-    auto sort_list = [&]() -> int {
-      const int n = min(sh.list_n, SAMPLE_LIST);
+    // The first CTA adds the CTAs' histograms and finds the bucket in which the
+    // count (after `above` tokens) reaches `want`, or the mass (after
+    // mass_above) reaches bar; a bar of 0 is set here, from the mass of all.
+    // Every CTA gets what was found; bucket -1: fewer than wanted.
+    auto find = [&](bool by_mass, u64 want, u64 above, u64 mass_above, u64 bar) -> SampleRow::Found {
+      cluster.sync();
+      if (rank == 0) {
+        u64 n[2] = {0, 0}, m[2] = {0, 0};
+        for (int r = 0; r < C; ++r) {
+          const uint32_t *rc = cluster.map_shared_rank(h_cnt, r);
+          const uint2 cnt = *reinterpret_cast<const uint2 *>(rc + 2 * tid);
+          n[0] += cnt.x;
+          n[1] += cnt.y;
+          if (by_mass) {
+            const uint2 lo = *reinterpret_cast<const uint2 *>(rc + SAMPLE_BUCKETS + 2 * tid);
+            const uint2 hi = *reinterpret_cast<const uint2 *>(rc + 2 * SAMPLE_BUCKETS + 2 * tid);
+            m[0] += ((u64)hi.x << 32) + lo.x;
+            m[1] += ((u64)hi.y << 32) + lo.y;
+          }
+        }
+        u64 tn, tm = 0, bm = 0;
+        const u64 bn = block_scan(n[0] + n[1], sh.red, tn);
+        if (by_mass) bm = block_scan(m[0] + m[1], sh.red, tm);
+        if (by_mass && bar == 0) {
+          bar = p > 0.0 ? (u64)ceil(p * (double)tm) : 1;
+          if (bar < 1) bar = 1;
+        }
+        if (!by_mass && tid == 0 && above + tn < want) sh.found.bucket = -1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const u64 pn = above + bn + (i ? n[0] : 0), pm = mass_above + bm + (i ? m[0] : 0);
+          const bool here = by_mass ? pm < bar && bar <= pm + m[i] : pn < want && want <= pn + n[i];
+          if (here)
+            sh.found = SampleRow::Found{2 * tid + i, (int)n[i], pn, pm, pn + n[i], bar, 0, 0, 0.f};
+        }
+      }
+      cluster.sync();
+      return *lead;
+    };
+    // a token to the first CTA's list
+    auto push = [&](float l, int v) {
+      const int at = atomicAdd(lead_n, 1);
+      if (at < SAMPLE_LIST) lead_list[at] = ((u64)logit_key(l) << 32) | (uint32_t)~(uint32_t)v;
+    };
+    // first CTA: the list's first n words in descending order
+    auto sort_list = [&](int n) {
       int m = 32;
       while (m < n) m <<= 1;
       for (int i = n + tid; i < m; i += SAMPLE_THREADS) list[i] = 0;
-      for (int size = 2; size <= m; size <<= 1)
+      if (m <= 128) {                            // ranks by counting, four threads to a word
+        __syncthreads();
+        u64 x = 0;
+        int r = 0;
+        if (tid < 4 * m) {
+          x = list[tid >> 2];
+          for (int i = tid & 3; i < m; i += 4) {
+            const u64 y = list[i];
+            r += y > x || (y == x && i < (tid >> 2));
+          }
+        }
+        r += __shfl_xor_sync(FULL, r, 1);
+        r += __shfl_xor_sync(FULL, r, 2);
+        __syncthreads();
+        if (tid < 4 * m && (tid & 3) == 0) list[r] = x;
+        __syncthreads();
+        return;
+      }
+      for (int size = 2; size <= m; size <<= 1)  // a bitonic network
         for (int d = size >> 1; d > 0; d >>= 1) {
           __syncthreads();
           for (int i = tid; i < m / 2; i += SAMPLE_THREADS) {
@@ -340,101 +426,204 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           }
         }
       __syncthreads();
-      return n;
+    };
+    auto listed = [&](int i) { return key_logit((uint32_t)(list[i] >> 32)); };
+    // first CTA: of the sorted list's first n tokens, the index of the last that
+    // top-p keeps, once `need` is the mass wanted (0: top_p of all n)
+    auto last_by_mass = [&](int n, u64 need, u64 (&m)[2]) -> int {
+      u64 total;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[i] = 2 * tid + i < n ? mass_at(listed(2 * tid + i)) : 0;
+      const u64 before = block_scan(m[0] + m[1], sh.red, total);
+      if (need == 0) need = p > 0.0 ? (u64)ceil(p * (double)total) : 1;
+      if (need < 1) need = 1;
+      if (tid == 0) sh.pos = n - 1;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const u64 pm = before + (i ? m[0] : 0);
+        if (pm < need && need <= pm + m[i]) sh.pos = 2 * tid + i;
+      }
+      __syncthreads();
+      return sh.pos;
     };
 
-    // One filter: the least prefix (of what is kept) with `want` tokens, or with
-    // a mass of top_p times all.  `all`: where few enough, every token of the
-    // prefix is listed and both filters are settled at once.
-    auto select = [&](bool by_mass, u64 want) -> bool {
-      const float scale =
-          by_mass ? (float)(c * (SAMPLE_BUCKETS - 1) / 40.0) : (float)(SAMPLE_BUCKETS - 1) / 32.f;
+    const float by_logit = (SAMPLE_BUCKETS - 1) / 32.f;       // 1024 buckets over 32 logits
+    auto level0 = [&](float l, float scale) {
+      return (int)fminf((top - l) * scale, (float)(SAMPLE_BUCKETS - 1));
+    };
+
+    // ---- top-k whose tokens fit the list: the first CTA settles the row ----
+    // For small k the histogram takes every thread's own maximum alone: the
+    // bucket of the k-th of those lies no higher than that of the k-th token.
+    bool counted = false;
+    SampleRow::Found f{};
+    if (by_k && k <= SAMPLE_LIST) {
+      bool fits = false;
+      if (k <= SAMPLE_SMALL_K && !inf_row) {
+        clear();
+        if (most > -INFINITY) atomicAdd(h_cnt + level0(canonical(most), by_logit), 1u);
+        f = find(false, (u64)k, 0, 0, 0);
+        fits = f.bucket >= 0;
+      }
+      if (!fits) {
+        clear();
+        for_kept([&](float l, int) { atomicAdd(h_cnt + level0(l, by_logit), 1u); });
+        f = find(false, (u64)k, 0, 0, 0);
+        counted = true;
+        fits = f.bucket >= 0 && f.upto <= SAMPLE_LIST;
+      }
+      if (fits) {
+        for_kept([&](float l, int v) {
+          if (level0(l, by_logit) <= f.bucket) push(l, v);
+        });
+        cluster.sync();
+        const int n = *lead_n;
+        cluster.barrier_arrive();                // (the list's length is read)
+        if (n <= SAMPLE_LIST) {
+          if (rank == 0) {
+            sort_list(n);
+            u64 m[2];
+            const int nk = min(n, k);
+            const int last = last_by_mass(nk, by_p ? 0 : ~0ull, m);
+            double w = 0.0;
+            u64 mine = 0, total;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 2 * tid + i;
+              if (r > last || (r > 0 && m[i] < low)) m[i] = 0;
+              else if (z.positive(listed(r))) w += z.weight(listed(r));
+              mine += m[i];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(FULL, w, o);
+            if (lane == 0) sh.redd[warp] = w;
+            block_scan(mine, sh.red, total);     // (its barriers order sh.redd)
+            w = 0.0;
+            for (int j = 0; j < SAMPLE_WARPS; ++j) w += sh.redd[j];
+            if (tid == 0) {
+              const u64 e = list[last];
+              sh.found.thr = (uint32_t)(e >> 32);
+              sh.found.cut = (int)~(uint32_t)e;
+              sh.found.inv = (float)(1.0 / w);
+            }
+            if (a.token) {                       // the draw, along the indices
+              u64 *const ms = reinterpret_cast<u64 *>(h_cnt);
+              ms[2 * tid] = m[0];
+              ms[2 * tid + 1] = m[1];
+              __syncthreads();
+              for (int r = tid; r <= last; r += SAMPLE_THREADS)    // ~index above, place below
+                list[r] = (list[r] << 32) | (uint32_t)r;
+              sort_list(last + 1);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                m[i] = 2 * tid + i <= last ? ms[(uint32_t)list[2 * tid + i]] : 0;
+              u64 run = block_scan(m[0] + m[1], sh.red, total);
+              const u64 U = (u64)((double)__ldg(a.u + row) * 16777216.0);
+              const u64 want = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (run <= want && want < run + m[i])
+                  a.token[row] = (int)~(uint32_t)(list[2 * tid + i] >> 32);
+                run += m[i];
+              }
+            }
+          }
+          cluster.barrier_wait();
+          if (!probs) return;
+          cluster.sync();
+          thr = lead->thr;
+          cut = lead->cut;
+          const float inv = lead->inv, at = key_logit(thr);
+          cluster.barrier_arrive();              // (read before the first CTA leaves)
+          write_probs([&](int j) {
+            const float4 q = val4[j];
+            float e[4] = {q.x, q.y, q.z, q.w};
+            const bool any = e[0] >= at || e[1] >= at || e[2] >= at || e[3] >= at;
+            if (!any) return make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float pv = 0.f;
+              if ((e[i] > at || (e[i] == at && v0 + 4 * j + i <= cut)) && z.positive(e[i])) {
+                const double w = z.weight(e[i]);
+                if (sample_mass(w) >= low) pv = (float)w * inv;
+              }
+              e[i] = pv;
+            }
+            return make_float4(e[0], e[1], e[2], e[3]);
+          });
+          cluster.barrier_wait();
+          return;
+        }
+        cluster.barrier_wait();
+      }
+    }
+
+    // ---- one filter: the least prefix of what is kept with `want` tokens, or
+    // with top_p of its mass ----
+    auto select = [&](bool by_mass, u64 want) {
+      const float scale = by_mass ? z.fc * ((SAMPLE_BUCKETS - 1) / 40.f) : by_logit;
       uint32_t khi = 0xffffffffu, klo = 0;       // keys in question
       int bits = -1;                             // bucket width, or the first level's scale
       u64 above = 0, mass_above = 0, bar = 0;
+      bool have = !by_mass && counted;           // the first level is there already
       for (;;) {
-        auto bucket_of = [&](float l, uint32_t key) -> int {
-          if (bits >= 0) return (int)((khi - key) >> bits);
-          return l == top ? 0 : (int)fminf((top - l) * scale, (float)(SAMPLE_BUCKETS - 1));
+        // the bucket of a logit, -1 if it is not in question any more
+        auto bucket_of = [&](float l) -> int {
+          if (bits < 0) return level0(l, scale);
+          const uint32_t key = logit_key(l);
+          return key < klo || key > khi ? -1 : (int)((khi - key) >> bits);
         };
-        for (int i = tid; i < SAMPLE_BUCKETS; i += SAMPLE_THREADS) h_cnt[i] = h_lo[i] = h_hi[i] = 0;
-        if (tid == 0) sh.list_n = 0;
-        __syncthreads();
-        for_kept([&](float l, uint32_t key, int) {
-          if (key < klo || key > khi) return;
-          const int b = bucket_of(l, key);
-          atomicAdd(h_cnt + b, 1u);
+        if (!have) {
+          clear();
           if (by_mass) {
-            const u64 m = sample_mass(weight(l));
-            const uint32_t lo = (uint32_t)m, old = atomicAdd(h_lo + b, lo);
-            const uint32_t hi = (uint32_t)(m >> 32) + (old + lo < old ? 1u : 0u);
-            if (hi) atomicAdd(h_hi + b, hi);
-          }
-        });
-        cluster.sync();
-        if (rank == 0) {                         // add the CTAs' histograms, find the bucket
-          u64 n[2] = {0, 0}, m[2] = {0, 0};
-          for (int r = 0; r < C; ++r) {
-            const uint32_t *rc = cluster.map_shared_rank(h_cnt, r);
+            for (int j = tid; j < units; j += SAMPLE_THREADS) {
+              const float4 q = val4[j];
+              const float e[4] = {q.x, q.y, q.z, q.w};
+              u64 m[4];
+              // the four weights side by side: a double's latency is that of
+              // many others
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              n[i] += rc[2 * tid + i];
-              if (by_mass)
-                m[i] += ((u64)rc[2 * SAMPLE_BUCKETS + 2 * tid + i] << 32) + rc[SAMPLE_BUCKETS + 2 * tid + i];
+              for (int i = 0; i < 4; ++i) m[i] = sample_mass(z.weight(e[i]));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (!(e[i] == e[i])) continue;
+                if (thr) {
+                  const uint32_t key = logit_key(e[i]);
+                  if (key < thr || (key == thr && v0 + 4 * j + i > cut)) continue;
+                }
+                const int b = bucket_of(e[i]);
+                if (b < 0) continue;
+                atomicAdd(h_cnt + b, 1u);
+                if (!z.positive(e[i])) continue;
+                const uint32_t lo = (uint32_t)m[i], old = atomicAdd(h_lo + b, lo);
+                const uint32_t hi = (uint32_t)(m[i] >> 32) + (old + lo < old ? 1u : 0u);
+                if (hi) atomicAdd(h_hi + b, hi);
+              }
             }
+          } else {
+            for_kept([&](float l, int) {
+              const int b = bucket_of(l);
+              if (b >= 0) atomicAdd(h_cnt + b, 1u);
+            });
           }
-          u64 tn, tm = 0, bm = 0;
-          const u64 bn = block_scan(n[0] + n[1], sh.red, tn);
-          if (by_mass) bm = block_scan(m[0] + m[1], sh.red, tm);
-          if (by_mass && bits < 0) {             // (the first level sees every kept token)
-            bar = p > 0.0 ? (u64)ceil(p * (double)tm) : 1;
-            if (bar < 1) bar = 1;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const u64 pn = above + bn + (i ? n[0] : 0), pm = mass_above + bm + (i ? m[0] : 0);
-            const bool here = by_mass ? pm < bar && bar <= pm + m[i] : pn < want && want <= pn + n[i];
-            if (here)
-              sh.found = SampleRow::Found{2 * tid + i, (int)n[i], pn, pm, pn + n[i], bar, 0, 0};
-          }
+          f = find(by_mass, want, above, mass_above, bar);
         }
-        cluster.sync();
-        const SampleRow::Found f = *lead;
+        have = false;
+        if (f.bucket < 0) return;                // fewer tokens than wanted (the rest is NaN)
         bar = f.bar;
-        const bool all = !by_mass && bits < 0 && f.upto <= SAMPLE_LIST;
-        if (all || f.count <= SAMPLE_LIST) {
-          for_kept([&](float l, uint32_t key, int v) {
-            if (key < klo || key > khi) return;
-            const int b = bucket_of(l, key);
-            push(all ? b <= f.bucket : b == f.bucket, key, v);
+        if (f.count <= SAMPLE_LIST) {
+          cluster.sync();                        // (found is read; it takes the answer)
+          for_kept([&](float l, int v) {
+            if (bucket_of(l) == f.bucket) push(l, v);
           });
           cluster.sync();
           if (rank == 0) {
-            const int n = sort_list();
-            int last;                            // the list's last kept token
-            if (!by_mass && !(all && by_p)) {
-              last = (int)(want - (all ? 0 : f.above)) - 1;
-            } else {
-              // masses along the list: two tokens to a thread
-              const int nk = by_mass ? n : min(n, (int)want);
-              u64 m[2], total;
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                m[i] = 2 * tid + i < nk ? sample_mass(weight(key_logit((uint32_t)(list[2 * tid + i] >> 32)))) : 0;
-              const u64 before = block_scan(m[0] + m[1], sh.red, total);
-              u64 need = by_mass ? bar - f.mass_above
-                                 : (p > 0.0 ? (u64)ceil(p * (double)total) : 1);
-              if (need < 1) need = 1;
-              if (tid == 0) sh.pos = nk - 1;
-              __syncthreads();
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const u64 pm = before + (i ? m[0] : 0);
-                if (pm < need && need <= pm + m[i]) sh.pos = 2 * tid + i;
-              }
-              __syncthreads();
-              last = sh.pos;
-            }
+            const int n = min(sh.list_n, SAMPLE_LIST);
+            sort_list(n);
+            u64 m[2];
+            const int last =
+                by_mass ? last_by_mass(n, bar - f.mass_above, m) : (int)(want - f.above) - 1;
             if (tid == 0) {
               const u64 e = list[max(0, min(last, n - 1))];
               sh.found.thr = (uint32_t)(e >> 32);
@@ -445,15 +634,16 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           thr = lead->thr;
           cut = lead->cut;
           cluster.sync();                        // (found is free for the next filter)
-          return all;
+          return;
         }
         // more tokens than the list holds: the keys of this bucket
         above = f.above;
         mass_above = f.mass_above;
         if (bits < 0) {
           u64 hi = 0, lo = 0;
-          for_kept([&](float l, uint32_t key, int) {
-            if (bucket_of(l, key) != f.bucket) return;
+          for_kept([&](float l, int) {
+            if (bucket_of(l) != f.bucket) return;
+            const uint32_t key = logit_key(l);
             hi = key > hi ? key : hi;
             lo = (uint32_t)~key > lo ? (uint32_t)~key : lo;
           });
@@ -465,10 +655,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           klo = khi - klo > width ? khi - width : klo;
         }
         if (khi == klo) {                        // equal logits: cut by count
-          const u64 one = by_mass ? sample_mass(weight(key_logit(khi))) : 1;
+          const u64 one = by_mass ? mass_at(key_logit(khi)) : 1;
           const u64 take = by_mass ? (bar - mass_above + one - 1) / one : want - above;
           u64 mine = 0;
-          for_kept([&](float, uint32_t key, int) { mine += key == khi; });
+          for_kept([&](float l, int) { mine += logit_key(l) == khi; });
           u64 cnt;
           block_scan(mine, sh.red, cnt);
           const u64 *pc = exchange(cnt);
@@ -506,16 +696,14 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           for (int j = 0; j < C; ++j) sum += pa[j];
           thr = khi;
           cut = (int)sum - 1;
-          return false;
+          return;
         }
         const int width = 32 - __clz(khi - klo);   // bits of the distance
         bits = width > 10 ? width - 10 : 0;
       }
     };
-
-    bool settled = false;
-    if (by_k) settled = select(false, (u64)k);
-    if (by_p && !settled) select(true, 0);
+    if (by_k) select(false, (u64)k);
+    if (by_p) select(true, 0);
   }
 
   // ---- sums over what is kept; warp w takes the w-th part of the slice ----
@@ -524,29 +712,31 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   double wsum = 0.0;
   {
     const int j1 = min(units, (warp + 1) * wu);
-    const float below = (float)(-1000.0 / c);
-    for (int j = warp * wu + lane; j < j1; j += 32) {
-      const float4 q = val4[j];
-      float e[4] = {q.x, q.y, q.z, q.w};
+    // kept(l, v): whether the threshold keeps a token
+    auto sums = [&](auto kept) {
+      for (int j = warp * wu + lane; j < j1; j += 32) {
+        const float4 q = val4[j];
+        float e[4] = {q.x, q.y, q.z, q.w};
+        double w[4];
+        u64 m[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float keep = 0.f;
-        if (e[i] == e[i] && (e[i] == top || e[i] - top > below)) {
-          const uint32_t key = logit_key(e[i]);
-          if (key > thr || (key == thr && v0 + 4 * j + i <= cut)) {
-            const double w = weight(e[i]);
-            const u64 m = sample_mass(w);
-            if (m >= low) {
-              mass += m;
-              wsum += w;
-              keep = (float)w;
-            }
-          }
+        for (int i = 0; i < 4; ++i) w[i] = z.weight(e[i]);          // (side by side)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          m[i] = sample_mass(w[i]);
+          const bool keep = z.positive(e[i]) && kept(e[i], v0 + 4 * j + i) && m[i] >= low;
+          mass += keep ? m[i] : 0;
+          wsum += keep ? w[i] : 0.0;
+          e[i] = keep ? (float)w[i] : 0.f;
         }
-        e[i] = keep;
+        if (probs) val4[j] = make_float4(e[0], e[1], e[2], e[3]);   // weights, for the probabilities
       }
-      if (probs) val4[j] = make_float4(e[0], e[1], e[2], e[3]);     // weights, for the probabilities
-    }
+    };
+    const float at = key_logit(thr);             // (thr 0, nothing cut: NaN)
+    if (thr)
+      sums([&](float l, int v) { return l > at || (l == at && v <= cut); });
+    else
+      sums([](float, int) { return true; });
   }
   mass = warp_sum_u64(mass);
 #pragma unroll
@@ -597,10 +787,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const int each = (b1 - b0 + SAMPLE_THREADS - 1) / SAMPLE_THREADS;
   const int t0 = min(b1, b0 + tid * each), t1 = min(b1, t0 + each);
   auto mass_of = [&](int v) -> u64 {
-    const float l = canonical(x[v]);
+    const float l = infinite(canonical(x[v]));
     const uint32_t key = logit_key(l);
     if (key < thr || (key == thr && v > cut)) return 0;
-    const u64 mv = sample_mass(weight(l));
+    const u64 mv = mass_at(l);
     return mv >= low ? mv : 0;
   };
   u64 mine = 0, all;
