@@ -31,6 +31,7 @@
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
+#include <type_traits>
 #include "common.cuh"
 
 namespace moe {
@@ -57,25 +58,23 @@ struct SampleArgs {
   int slice;                     // tokens of a CTA, a multiple of 4
 };
 
-// In shared memory a logit is canonical: -0 becomes 0; NaN, which also fills
-// the places outside the row, stays and counts as no token at all.
-__device__ __forceinline__ float canonical(float x) { return x + 0.f; }
-
-// order-preserving key of a canonical logit
+// order-preserving key of a logit, -0 as 0.  (NaN counts as no token at all; in
+// shared memory it also fills the places outside the row.)
 __device__ __forceinline__ uint32_t logit_key(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// w = 2^(d c), d = x - top <= 0, c = log2(e) / temperature, for d c > -1000 (the
-// caller takes 0 for less).  The exponent's nearest integer comes from float (it
-// need not be exact: the remainder f is), 2^f on [-1/2, 1/2] is 1 + f p(f), p of
-// degree 7 fitted to the least relative error at Chebyshev nodes: 2^-40, the
-// masses' own step.  11 double operations and two conversions.  (Temperatures
-// below 1e-36 count as 1e-36, so that the scale stays finite in float.)
+// 2^40 w = 2^(d c + 40), d = x - top <= 0, c = log2(e) / temperature, for
+// d c > -1000 (the caller takes 0 for less).  The exponent's nearest integer
+// comes from float (it need not be exact: the remainder f is), 2^f on
+// [-1/2, 1/2] is 1 + f p(f), p of degree 7 fitted to the least relative error
+// at Chebyshev nodes: 2^-40, the masses' own step.  11 double operations and
+// two conversions.  Temperatures below 1e-36 count as 1e-36, so that the scale
+// stays finite in float.
 struct SampleScale {
   double top, c;
   float ftop, fc, below;          // weights of x - top <= below are 0
@@ -84,7 +83,7 @@ struct SampleScale {
         below(fmaxf((float)(-1000.0 / c), -FLT_MAX)) {}
   __device__ __forceinline__ bool positive(float x) const { return x - ftop > below; }   // NaN: no
   __device__ __forceinline__ double weight(float x) const {
-    const float magic = 12582912.f;                                 // 1.5 2^23
+    const float magic = 12582912.f + 40.f;                          // 1.5 2^23, and the 2^40
     const float shifted = fmaf(x - ftop, fc, magic);
     const double f = fma((double)x - top, c, -(double)(shifted - magic));
     double p = 1.318882399508972e-06;
@@ -99,11 +98,15 @@ struct SampleScale {
     return __hiloint2double(__double2hiint(p) + (__float_as_int(shifted) << 20), __double2loint(p));
   }
 };
-// floor(w 2^40), 2^-1000 < w <= 1: added to 2^52 the integer part is the low bits
-__device__ __forceinline__ unsigned long long sample_mass(double w) {
-  const double scaled = __hiloint2double(__double2hiint(w) + (40 << 20), __double2loint(w));
-  return (unsigned long long)__double_as_longlong(__dadd_rd(scaled, 4503599627370496.0)) &
-         0xfffffffffffffull;
+// floor(2^40 w), 2^-960 < 2^40 w <= 2^40: added to 2^52 the integer part is the
+// low 52 bits (the high 12 are left to the caller to mask: sums of masses below
+// 2^52 stay apart from them)
+constexpr unsigned long long SAMPLE_MASK = 0xfffffffffffffull;
+__device__ __forceinline__ unsigned long long sample_mass_bits(double w40) {
+  return (unsigned long long)__double_as_longlong(__dadd_rd(w40, 4503599627370496.0));
+}
+__device__ __forceinline__ unsigned long long sample_mass(double w40) {
+  return sample_mass_bits(w40) & SAMPLE_MASK;
 }
 
 // A cluster's view of one row, and the block- and cluster-wide sums.
@@ -116,7 +119,7 @@ struct SampleRow {
     u64 bar;                   // top-p's mass
     uint32_t thr;
     int cut;
-    float inv;                 // 1 / sum of the kept weights, where the list settles a row
+    float inv;                 // 2^-40 / sum of the kept weights, where the list settles a row
   };
   struct Shared {
     u64 xch[8][SAMPLE_MAX_CLUSTER];
@@ -142,6 +145,12 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     v = w > v ? w : v;
   }
   return v;
+}
+__device__ __forceinline__ void sample_copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
 }
 // exclusive prefix of a value over the block's threads, and the block's total
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
@@ -219,35 +228,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     return m;
   };
 
-  // ---- the slice into shared memory; the largest logit ----
-  float most = -INFINITY;
-  {
-    constexpr int U = 4;
-    const float none = __int_as_float(0x7fffffff);
-    for (int j = tid; j < units; j += U * SAMPLE_THREADS) {
-      float4 q[U];
+  // ---- the slice into shared memory, all of it in flight at once; a
+  // sequence's settings meanwhile ----
+  for (int j = tid; j < units; j += SAMPLE_THREADS) {
+    const int v = v0 + 4 * j;
+    if (v >= c0 && v + 3 < c1) {
+      sample_copy16(val4 + j, x + v);
+    } else {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int unit = j + i * SAMPLE_THREADS, v = v0 + 4 * unit;
-        if (unit >= units) break;
-        if (v >= c0 && v + 3 < c1) {
-          q[i] = __ldcs(reinterpret_cast<const float4 *>(x + v));
-        } else {
-          q[i].x = v >= c0 && v < c1 ? x[v] : none;
-          q[i].y = v + 1 >= c0 && v + 1 < c1 ? x[v + 1] : none;
-          q[i].z = v + 2 >= c0 && v + 2 < c1 ? x[v + 2] : none;
-          q[i].w = v + 3 >= c0 && v + 3 < c1 ? x[v + 3] : none;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int unit = j + i * SAMPLE_THREADS;
-        if (unit >= units) break;
-        q[i] = make_float4(canonical(q[i].x), canonical(q[i].y), canonical(q[i].z), canonical(q[i].w));
-        val4[unit] = q[i];
-        most = fmaxf(most, fmaxf(fmaxf(q[i].x, q[i].y), fmaxf(q[i].z, q[i].w)));   // (skips NaN)
-      }
+      for (int i = 0; i < 4; ++i)
+        val[4 * j + i] = v + i >= c0 && v + i < c1 ? x[v + i] : __int_as_float(0x7fffffff);
     }
+  }
+  const double T = a.temperature ? (double)__ldg(a.temperature + s) : 1.0;
+  const int k = a.top_k ? __ldg(a.top_k + s) : 0;
+  const double p = a.top_p ? (double)__ldg(a.top_p + s) : 1.0;
+  const float mp = a.min_p ? __ldg(a.min_p + s) : 0.f;
+  const u64 U = a.token ? (u64)((double)__ldg(a.u + row) * 16777216.0) : 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // (each thread reads back what it copied itself)
+  float most = -INFINITY;
+  for (int j = tid; j < units; j += SAMPLE_THREADS) {
+    const float4 q = val4[j];
+    most = fmaxf(most, fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));    // (skips NaN)
   }
   cluster.barrier_wait();
   float top = key_logit((uint32_t)cluster_max(logit_key(most)));
@@ -280,7 +283,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       }
     }
   };
-  const double T = a.temperature ? (double)__ldg(a.temperature + s) : 1.0;
   const bool none = top == -INFINITY;
   if (none || !(T > 0.0)) {                       // no mass, or the first-ranked token alone
     uint32_t first = 0;                           // ~index of the first largest logit
@@ -313,10 +315,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // ---- the threshold: kept are keys above thr, and at thr the tokens <= cut ----
   uint32_t thr = 0;
   int cut = 0x7fffffff;
-  const int k = a.top_k ? __ldg(a.top_k + s) : 0;
-  const double p = a.top_p ? (double)__ldg(a.top_p + s) : 1.0;
   const bool by_k = k > 0 && k < V, by_p = p < 1.0;
-  const float mp = a.min_p ? __ldg(a.min_p + s) : 0.f;
   const u64 low = mp > 0.f ? (u64)((double)fminf(mp, 1.f) * (double)SAMPLE_ONE) : 0;
 
   if (by_k || by_p) {
@@ -462,7 +461,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       bool fits = false;
       if (k <= SAMPLE_SMALL_K && !inf_row) {
         clear();
-        if (most > -INFINITY) atomicAdd(h_cnt + level0(canonical(most), by_logit), 1u);
+        if (most > -INFINITY) atomicAdd(h_cnt + level0(most, by_logit), 1u);
         f = find(false, (u64)k, 0, 0, 0);
         fits = f.bucket >= 0;
       }
@@ -519,7 +518,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
               for (int i = 0; i < 2; ++i)
                 m[i] = 2 * tid + i <= last ? ms[(uint32_t)list[2 * tid + i]] : 0;
               u64 run = block_scan(m[0] + m[1], sh.red, total);
-              const u64 U = (u64)((double)__ldg(a.u + row) * 16777216.0);
               const u64 want = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -712,31 +710,44 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   double wsum = 0.0;
   {
     const int j1 = min(units, (warp + 1) * wu);
-    // kept(l, v): whether the threshold keeps a token
-    auto sums = [&](auto kept) {
+    // kept(l, v): whether the threshold keeps a token.  A thread's masses add up
+    // below 2^52, so the bits above are dropped once at the end.
+    auto sums = [&](auto with_probs, auto least, auto kept) {
       for (int j = warp * wu + lane; j < j1; j += 32) {
         const float4 q = val4[j];
         float e[4] = {q.x, q.y, q.z, q.w};
         double w[4];
-        u64 m[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = z.weight(e[i]);          // (side by side)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          m[i] = sample_mass(w[i]);
-          const bool keep = z.positive(e[i]) && kept(e[i], v0 + 4 * j + i) && m[i] >= low;
-          mass += keep ? m[i] : 0;
-          wsum += keep ? w[i] : 0.0;
-          e[i] = keep ? (float)w[i] : 0.f;
+          const u64 m = sample_mass_bits(w[i]);
+          bool keep = z.positive(e[i]) && kept(e[i], v0 + 4 * j + i);
+          if constexpr (decltype(least)::value) keep = keep && (m & SAMPLE_MASK) >= low;
+          if (keep) mass += m;
+          if constexpr (decltype(with_probs)::value) {
+            if (keep) wsum += w[i];
+            e[i] = keep ? (float)w[i] : 0.f;
+          }
         }
-        if (probs) val4[j] = make_float4(e[0], e[1], e[2], e[3]);   // weights, for the probabilities
+        if constexpr (decltype(with_probs)::value)                  // weights, for the probabilities
+          val4[j] = make_float4(e[0], e[1], e[2], e[3]);
       }
     };
-    const float at = key_logit(thr);             // (thr 0, nothing cut: NaN)
-    if (thr)
-      sums([&](float l, int v) { return l > at || (l == at && v <= cut); });
-    else
-      sums([](float, int) { return true; });
+    const std::true_type yes;
+    const std::false_type no;
+    if (thr || low) {
+      const float at = thr ? key_logit(thr) : -INFINITY;            // (thr 0: nothing cut)
+      const int last = thr ? cut : 0x7fffffff;
+      auto kept = [&](float l, int v) { return l > at || (l == at && v <= last); };
+      if (probs) sums(yes, yes, kept);
+      else sums(no, yes, kept);
+    } else {
+      auto kept = [](float, int) { return true; };
+      if (probs) sums(yes, no, kept);
+      else sums(no, no, kept);
+    }
+    mass &= SAMPLE_MASK;
   }
   mass = warp_sum_u64(mass);
 #pragma unroll
@@ -775,7 +786,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   if (!a.token) return;
 
   // ---- the draw: the CTA, the warp's part, then a few tokens to a thread ----
-  const u64 U = (u64)((double)__ldg(a.u + row) * 16777216.0);
   const u64 m = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
   if (!(before <= m && m < before + cta_mass)) return;
   int part = 0;
@@ -787,7 +797,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const int each = (b1 - b0 + SAMPLE_THREADS - 1) / SAMPLE_THREADS;
   const int t0 = min(b1, b0 + tid * each), t1 = min(b1, t0 + each);
   auto mass_of = [&](int v) -> u64 {
-    const float l = infinite(canonical(x[v]));
+    // (weights took the logits' place in shared memory where probabilities are wanted)
+    const float l = probs ? infinite(x[v]) : val[v - v0];
     const uint32_t key = logit_key(l);
     if (key < thr || (key == thr && v > cut)) return 0;
     const u64 mv = mass_at(l);
