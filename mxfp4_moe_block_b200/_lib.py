@@ -327,32 +327,48 @@ def mxfp4_quantize(w, codes=None, scales=None, stream=None):
 class _On:
     """The device and stream of a call: every tensor given lies on one CUDA
     device, which is current inside the context; outputs and scratch allocated
-    there belong to the stream the kernels run on."""
+    there belong to the stream the kernels run on.  (Nothing is switched for a
+    call on the current device and stream.)"""
+    __slots__ = ("device", "stream", "_ctx")
 
-    def __init__(self, stream, **tensors):
-        devs = {t.device for t in tensors.values() if t is not None}
-        bad = [n for n, t in tensors.items() if t is not None and not t.is_cuda]
-        if bad:
-            raise ValueError(f"{bad[0]} must be a CUDA tensor")
-        if len(devs) != 1:
-            raise ValueError("tensors on different devices: "
-                             + ", ".join(f"{n} {t.device}" for n, t in tensors.items() if t is not None))
-        self.device = devs.pop()
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if self.stream.device != self.device:
-            raise ValueError(f"stream of {self.stream.device} for tensors on {self.device}")
-        self._ctx = torch.cuda.stream(self.stream)     # also makes its device current
+    def __init__(self, stream, names, *tensors):
+        index = None
+        for t in tensors:
+            if t is not None:
+                i = t.get_device()
+                if i < 0 or i != index:
+                    if i < 0:
+                        bad = next(n for n, t in zip(names, tensors) if t is not None and not t.is_cuda)
+                        raise ValueError(f"{bad} must be a CUDA tensor")
+                    if index is not None:
+                        raise ValueError("tensors on different devices: " + ", ".join(
+                            f"{n} {t.device}" for n, t in zip(names, tensors) if t is not None))
+                    index = i
+                    self.device = t.device
+        here = index == torch.cuda.current_device()
+        self._ctx = None
+        if stream is None:
+            stream = torch.cuda.current_stream(index)
+            if not here:
+                self._ctx = torch.cuda.device(index)
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
+            self._ctx = torch.cuda.stream(stream)      # also makes its device current
+        self.stream = stream.cuda_stream
 
     def __enter__(self):
-        self._ctx.__enter__()
+        if self._ctx is not None:
+            self._ctx.__enter__()
         return self
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
 
 
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -361,8 +377,10 @@ def _cache_shapes(k_cache, v_cache, kv_len, block_table, S):
         raise ValueError("k_cache must be [pages, Hkv, page_size, D], block_table [S, max_pages]")
     _shape(v_cache, k_cache.shape, "v_cache")
     _shape(kv_len, (S,), "kv_len")
-    _shape(block_table, (S, block_table.shape[1]), "block_table")
-    return tuple(k_cache.shape) + (block_table.shape[1],)
+    rows, max_pages = block_table.shape
+    if rows != S:
+        raise ValueError(f"block_table must have {S} rows, got {rows}")
+    return (*k_cache.shape, max_pages)
 
 
 def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_weight=None,
@@ -373,17 +391,19 @@ def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_
     block_table [S, max_pages] int32; caches [pages, Hkv, page_size, D] bf16, updated in
     place; cos_sin [max_pos, rot] float or None (no rotation).  Returns q [S, N, Hq, D];
     rows of slots not in use are zero where the call allocates q, else left as they were."""
-    with _On(stream, qkv=qkv, kv_len=kv_len, block_table=block_table, k_cache=k_cache,
-             v_cache=v_cache, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight, q_out=q_out) as on:
+    with _On(stream, ("qkv", "kv_len", "block_table", "k_cache", "v_cache", "cos_sin", "q_weight",
+                      "k_weight", "q_out"), qkv, kv_len, block_table, k_cache, v_cache, cos_sin,
+             q_weight, k_weight, q_out) as on:
         S, N, heads, D = qkv.shape
-        pages, Hkv, page_size, _, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
-        _shape(k_cache, (pages, Hkv, page_size, D), "k_cache")
+        pages, Hkv, page_size, Dk, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
+        if Dk != D:
+            raise ValueError(f"k_cache must have heads of {D}, got {Dk}")
         Hq = heads - 2 * Hkv
         if q_out is None and Hq > 0:
             q_out = torch.zeros((S, N, Hq, D), dtype=torch.bfloat16, device=on.device)
         _shape(q_out, (S, N, Hq, D), "q_out")
-        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _shape(w, (D,), name)
+        _shape(q_weight, (D,), "q_weight")
+        _shape(k_weight, (D,), "k_weight")
         max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
         _check(lib().block_kv_append(
             _ptr(qkv, torch.bfloat16, "qkv"), S, N, Hq, Hkv, D, int(norm),
@@ -392,7 +412,7 @@ def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_
             _ptr(kv_len, torch.int32, "kv_len"), _ptr(block_table, torch.int32, "block_table"),
             max_pages, _ptr(k_cache, torch.bfloat16, "k_cache"),
             _ptr(v_cache, torch.bfloat16, "v_cache"), pages, page_size,
-            _ptr(q_out, torch.bfloat16, "q_out"), _stream(on.stream)), "block_kv_append")
+            _ptr(q_out, torch.bfloat16, "q_out"), on.stream), "block_kv_append")
     return q_out
 
 
@@ -410,11 +430,12 @@ def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window
     """Attention of N tokens per sequence over the paged cache; q [S, N, Hq, D] bf16.
 
     scale defaults to D ** -0.5; window 0 sees the whole cache.  Returns out [S, N, Hq, D]."""
-    with _On(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_len=kv_len,
-             out=out, workspace=workspace) as on:
+    with _On(stream, ("q", "k_cache", "v_cache", "block_table", "kv_len", "out", "workspace"),
+             q, k_cache, v_cache, block_table, kv_len, out, workspace) as on:
         S, N, Hq, D = q.shape
-        pages, Hkv, page_size, _, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
-        _shape(k_cache, (pages, Hkv, page_size, D), "k_cache")
+        pages, Hkv, page_size, Dk, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
+        if Dk != D:
+            raise ValueError(f"k_cache must have heads of {D}, got {Dk}")
         if out is None:
             out = torch.empty_like(q)
         _shape(out, q.shape, "out")
@@ -426,7 +447,7 @@ def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window
             _ptr(block_table, torch.int32, "block_table"), max_pages,
             _ptr(kv_len, torch.int32, "kv_len"), float(D ** -0.5 if scale is None else scale),
             int(window), _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace"),
-            workspace.numel(), _stream(on.stream)), "block_attention")
+            workspace.numel(), on.stream), "block_attention")
     return out
 
 
@@ -436,12 +457,14 @@ def block_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p
 
     Tokens are drawn where u [S, K] is given; probabilities are written where
     with_probs is set or probs given.  The filters are [S] tensors or None (off)."""
-    with _On(stream, logits=logits, u=u, temperature=temperature, top_k=top_k, top_p=top_p,
-             min_p=min_p, token=token, probs=probs) as on:
+    with _On(stream, ("logits", "u", "temperature", "top_k", "top_p", "min_p", "token", "probs"),
+             logits, u, temperature, top_k, top_p, min_p, token, probs) as on:
         S, K, V = logits.shape
         _shape(u, (S, K), "u")
-        for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
-            _shape(t, (S,), name)
+        _shape(temperature, (S,), "temperature")
+        _shape(top_k, (S,), "top_k")
+        _shape(top_p, (S,), "top_p")
+        _shape(min_p, (S,), "min_p")
         if u is not None and token is None:
             token = torch.empty((S, K), dtype=torch.int32, device=on.device)
         if with_probs and probs is None:
@@ -453,7 +476,7 @@ def block_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p
             _ptr(logits, f32, "logits"), S, K, V, _ptr(temperature, f32, "temperature"),
             _ptr(top_k, torch.int32, "top_k"), _ptr(top_p, f32, "top_p"), _ptr(min_p, f32, "min_p"),
             _ptr(u, f32, "u"), _ptr(token, torch.int32, "token"), _ptr(probs, f32, "probs"),
-            _stream(on.stream)), "block_sample")
+            on.stream), "block_sample")
     return token, probs
 
 
