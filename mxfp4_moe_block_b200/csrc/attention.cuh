@@ -27,6 +27,11 @@
 // issuer, 5-8 producers: cp.async of 16-byte units, page by page, into a ring
 // of K and V tiles in the 128-byte swizzle; rows outside the sequence or on a
 // bad page are zero-filled and masked by a bit per key.
+//
+// Few rows would leave most lanes, and so most softmax warps, without work: up
+// to 32 rows (64) the queries stand in the 128 MMA rows four (two) times, lane
+// group g weighs the g-th quarter (half) of each tile's keys, its other weights
+// stay zero, and the groups' O, m and l are joined at the segment's end.
 // Every wait is bounded (MOE_DEV_TIMEOUT), as in the expert FFN.
 #pragma once
 #include "common.cuh"
@@ -36,8 +41,7 @@ namespace moe {
 
 constexpr int ATTN_MAX_CTAS = 148;
 constexpr int ATTN_ROWS = 128;
-constexpr int ATTN_THREADS = 288;
-constexpr int ATTN_PRODUCERS = 128;
+constexpr int ATTN_THREADS = 224;
 constexpr int ATTN_MASKS = 8;
 
 struct AttnArgs {
@@ -53,6 +57,9 @@ struct AttnArgs {
   uint16_t *out;                       // [S, N, Hq, D]
   // workspace: unnormalised O [2G][D/4][rows_cap] float4, (m, l) [2G][rows_cap],
   // one AttnSplit per piece
+  // keys of a tile, and what its first key is a multiple of: whole pages where
+  // the pages go by TMA (use_tma), else KT and 1
+  int tile_keys, align, use_tma;
   float4 *part_o;
   float2 *part_ml;
   struct AttnSplit *split;
@@ -65,14 +72,17 @@ struct AttnSplit {
   int s, kvh, rb, first, count;
 };
 
-template <int D>
+template <int D, int KS>
 struct AttnCfg {
   static constexpr int KT = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int NC = KT / KS;                  // keys of a tile to one softmax thread
+  static constexpr int RG = ATTN_ROWS / KS;           // rows of a lane group
   static constexpr int kSlot = KT * D * 2;            // one K or V tile
   static constexpr int kQ = ATTN_ROWS * D * 2;
-  static constexpr int kSlots = D == 64 ? 12 : D == 128 ? 6 : 5;
+  static constexpr int kScratch = KS > 1 ? 32768 : 0; // 64 dims of O for the groups' sum
+  static constexpr int kSlots = (D == 64 ? 12 : D == 128 ? 6 : 5) - kScratch / kSlot;
   static constexpr int kMisc = 2048;
-  static constexpr int kSmem = kQ + kSlots * kSlot + kMisc;
+  static constexpr int kSmem = kQ + kSlots * kSlot + kScratch + kMisc;
   // tensor memory columns: S x2, O, P x2 (two bf16 to a column)
   static constexpr uint32_t kS = 0, kO = D == 256 ? 256 : 2 * KT;
   static constexpr uint32_t kP = D == 256 ? 2 * KT : kO + D;
@@ -135,6 +145,16 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -163,25 +183,41 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
-// Visible keys of a sequence: [lo, n), in tiles from lo on; none for a slot not
-// in use or (reported) a length past the table's row.
+// 4 COUNT dims of a row, value(i) the i-th four: to out as bf16, or to a piece
+template <int COUNT, typename F>
+__device__ __forceinline__ void attn_store(bool whole, uint16_t *dst, float4 *part, int stride,
+                                           F value) {
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < COUNT; i += 2) {
+      const float4 x = value(i), y = value(i + 1);
+      *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(
+          cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w), cvt_bf16x2(y.x, y.y), cvt_bf16x2(y.z, y.w));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) part[(size_t)i * stride] = value(i);
+  }
+}
+
+// Visible keys of a sequence: [lo, n), in tiles from `start` on; none for a
+// slot not in use or (reported) a length past the table's row.
 struct AttnSeq {
-  int lo, n, tiles;
+  int lo, start, n, tiles;
 };
-template <int KT>
 __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int s) {
   const int n = __ldg(a.kv_len + s);
-  if (n <= 0) return AttnSeq{0, 0, 0};
+  if (n <= 0) return AttnSeq{0, 0, 0, 0};
   if (n > a.max_pages * a.page_size) {
     raise_status(MOE_DEV_BAD_INDEX);
-    return AttnSeq{0, 0, 0};
+    return AttnSeq{0, 0, 0, 0};
   }
   const int lo = a.window > 0 ? max(0, n - a.N - a.window + 1) : 0;
-  return AttnSeq{lo, n, (n - lo + KT - 1) / KT};
+  const int start = lo - lo % a.align;
+  return AttnSeq{lo, start, n, (n - start + a.tile_keys - 1) / a.tile_keys};
 }
 
 // A CTA's piece of the line of tiles, item by item.  Every role walks it alone.
-template <int KT>
 struct AttnWalk {
   unsigned long long base, pos, end;   // first tile of sequence s, next tile, end of the piece
   AttnSeq q;
@@ -193,7 +229,7 @@ struct AttnWalk {
     if (pos >= end) return false;
     while (pos >= base + (unsigned long long)q.tiles * units) {
       base += (unsigned long long)q.tiles * units;
-      q = attn_seq<KT>(a, ++s);
+      q = attn_seq(a, ++s);
     }
     const unsigned long long at = pos - base;
     const unsigned item = (unsigned)(at / (unsigned)q.tiles);
@@ -215,8 +251,9 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b, int w) {
   return below_b & ~below_a;
 }
 
-// true iff `v` holds on every producer thread (named barrier 1)
-__device__ __forceinline__ bool producers_all(bool v) {
+// true iff `v` holds on every softmax thread (named barrier 1), so that they
+// decide together to stay or leave
+__device__ __forceinline__ bool softmax_all(bool v) {
   uint32_t r;
   __syncwarp();
   asm volatile(
@@ -225,18 +262,21 @@ __device__ __forceinline__ bool producers_all(bool v) {
       : "=r"(r) : "r"((uint32_t)v) : "memory");
   return r != 0;
 }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <int D>
-__global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a) {
-  typedef AttnCfg<D> C;
+template <int D, int KS>
+__global__ void __launch_bounds__(ATTN_THREADS, 1)
+attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+            const AttnArgs a) {
+  typedef AttnCfg<D, KS> C;
   constexpr int KT = C::KT;
   typedef unsigned long long u64;
   extern __shared__ __align__(1024) uint8_t attn_smem[];
   uint8_t *const s_q = attn_smem;
   uint8_t *const s_ring = attn_smem + C::kQ;
-  uint8_t *const misc = s_ring + C::kSlots * C::kSlot;
-  uint32_t *const rowidx = reinterpret_cast<uint32_t *>(misc);                 // [2][128]
-  uint32_t *const masks = rowidx + 2 * 128;                                    // [8][4]
+  float4 *const scratch = reinterpret_cast<float4 *>(s_ring + C::kSlots * C::kSlot);
+  uint8_t *const misc = s_ring + C::kSlots * C::kSlot + C::kScratch;
+  uint32_t *const masks = reinterpret_cast<uint32_t *>(misc);                  // [8][4]
   uint64_t *const full = reinterpret_cast<uint64_t *>(masks + ATTN_MASKS * 4); // [kSlots]
   uint64_t *const empty = full + C::kSlots;                                    // [kSlots]
   uint64_t *const s_full = empty + C::kSlots;                                  // [2]
@@ -247,14 +287,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
   uint64_t *const drain = q_empty + 1;
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(drain + 1);
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drain + 1) + 1;
-  int *const s_start = reinterpret_cast<int *>(drain + 2);                     // sequence, tiles
+  int *const s_start = reinterpret_cast<int *>(drain + 2);                     // first sequence
+  uint32_t *const issued = reinterpret_cast<uint32_t *>(drain + 4);            // [2] K, V tiles
   u64 *const s_base = reinterpret_cast<u64 *>(drain + 3);
   u64 *const scan = reinterpret_cast<u64 *>(s_q);                              // before Q arrives
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, ATTN_PRODUCERS + 4);
+      mbar_init(full + i, 33);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -262,10 +303,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
       mbar_init(p_full + i, 128);
       mbar_init(pv_done + i, 1);
     }
-    mbar_init(q_full, ATTN_PRODUCERS + 4);
+    mbar_init(q_full, 33);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    issued[0] = issued[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 4) {
@@ -282,16 +324,23 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
   const int per = (a.S + ATTN_THREADS - 1) / ATTN_THREADS;
   const int q0 = min(a.S, tid * per), q1 = min(a.S, q0 + per);
   u64 mine = 0;
-  for (int s = q0; s < q1; ++s) mine += attn_seq<KT>(a, s).tiles;
-  scan[tid] = mine;
+  for (int s = q0; s < q1; ++s) mine += attn_seq(a, s).tiles;
+  u64 upto = mine;                                 // inclusive prefix over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 v = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) scan[warp] = upto;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  u64 before = 0, total = 0;
-  for (int i = 0; i < ATTN_THREADS; ++i) {
+  u64 before = upto - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < ATTN_THREADS / 32; ++i) {
     const u64 v = scan[i];
-    if (i < tid) before += v;
+    if (i < warp) before += v;
     total += v;
   }
   total *= units;
@@ -301,7 +350,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
     int s = q0;
     u64 base = before * units;
     for (;;) {
-      const u64 t = (u64)attn_seq<KT>(a, s).tiles * units;
+      const u64 t = (u64)attn_seq(a, s).tiles * units;
       if (start < base + t) break;
       base += t;
       ++s;
@@ -309,7 +358,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
     *s_start = s;
     *s_base = base;
     // the item that this piece's start cuts, if no earlier start does
-    const unsigned T = (unsigned)attn_seq<KT>(a, s).tiles;
+    const unsigned T = (unsigned)attn_seq(a, s).tiles;
     const unsigned item = (unsigned)((start - base) / T);
     const u64 from = base + (u64)item * T;
     AttnSplit sp{s, (int)(item / (unsigned)a.row_blocks), (int)(item % (unsigned)a.row_blocks),
@@ -321,103 +370,134 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
   if (tid == 0 && start >= stop) a.split[blockIdx.x] = AttnSplit{0, 0, 0, 0, 0};
   // sequences without a key: zeros
   for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
-    if (attn_seq<KT>(a, s).tiles) continue;
+    if (attn_seq(a, s).tiles) continue;
     uint4 *o = reinterpret_cast<uint4 *>(a.out + (size_t)s * a.N * a.Hq * D);
     for (int i = tid; i < a.N * a.Hq * (D / 8); i += ATTN_THREADS) o[i] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
 
   if (start < stop) {
-    AttnWalk<KT> w;
+    AttnWalk w;
     w.base = *s_base;
     w.pos = start;
     w.end = stop;
     w.s = *s_start;
-    w.q = attn_seq<KT>(a, w.s);
+    w.q = attn_seq(a, w.s);
+    // rows that a tile of whole pages leaves unused: their weights are 0, their
+    // values must not be NaN
+    if (a.tile_keys < KT)
+      for (int i = tid; i < C::kSlots * C::kSlot / 16; i += ATTN_THREADS)
+        reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
     __syncthreads();       // (the scan's memory becomes Q)
     const int group = a.Hq / a.Hkv;
 
     if (warp >= 5) {
-      // ---------------------------------------------------------- producers --
+      // ------------------------------------------ producers: K and (Q, then) V --
+      // A full tile of whole pages is a TMA box per page and 64 dims; a tile with
+      // keys outside [lo, n) or on a bad page, and pages that are no whole
+      // number of eight rows, go row by row through cp.async, which zero-fills
+      // what is outside.  Either way a slot's barrier gets 33 arrivals.
       constexpr int UNITS = D / 8;                     // 16-byte units of a row
-      constexpr int RPP = ATTN_PRODUCERS / UNITS;      // rows of one pass
-      const int p = tid - 160, u = p % UNITS, r0 = p / UNITS;
+      constexpr int RPP = 32 / UNITS;                  // rows of one pass of the warp
+      const bool is_k = warp == 5;
+      const int u = lane % UNITS, r0 = lane / UNITS;
       const uint32_t ring = smem_u32(s_ring);
+      const uint16_t *const cache = is_k ? a.k_cache : a.v_cache;
+      const CUtensorMap *const map = is_k ? &k_map : &v_map;
+      const uint64_t policy = policy_evict_normal();
       // unit u of row r in a tile of `rows` rows: 64-dim column blocks, swizzled
       auto place = [&](int r, int rows) -> uint32_t {
         return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
       };
-      uint32_t i = 0, t = 0, seg = 0;                  // ring index, tile, segment
+      const int boxes = a.use_tma ? max(1, a.tile_keys / a.page_size) : 0;   // pages of a tile
+      const int box_rows = a.use_tma ? a.tile_keys / boxes : 0;
+      // this lane's page of the tile whose first key is k0 (whole tiles only)
+      auto page_of = [&](const AttnWalk &w, int k0) -> int {
+        const int lp = k0 / a.page_size + lane;
+        if (lane >= boxes || k0 < w.q.lo || k0 + a.tile_keys > w.q.n) return -1;
+        return __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
+      };
+      uint32_t t = 0, seg = 0;                         // tile, segment
       bool ok = true;
-      auto slot_free = [&]() {
-        return i < (uint32_t)C::kSlots ||
-               attn_wait(empty + i % C::kSlots, (i / C::kSlots + 1) & 1, abort_flag);
-      };
-      auto load = [&](const uint16_t *cache, const uint32_t *rows) {
-        const uint32_t dst = ring + (i % C::kSlots) * C::kSlot;
-#pragma unroll
-        for (int j = 0; j < KT / RPP; ++j) {
-          const int r = r0 + j * RPP;
-          const uint32_t row = rows[r];
-          const bool live = row != 0xffffffffu;
-          cp_async16_zfill(dst + place(r, KT), cache + (live ? (size_t)row * D : 0) + u * 8, live);
-        }
-        cp_async_arrive_noinc(full + i % C::kSlots);
-        if (lane == 0) mbar_arrive(full + i % C::kSlots);
-        ++i;
-      };
-      // (the producers leave together: a wait that ran out is carried to the
-      // next tile's barrier)
-      bool leave = false;
-      while (!leave && w.next(a, units)) {
-        const int32_t *table = a.block_table + (size_t)w.s * a.max_pages;
-        for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
-          ok = slot_free() && ok;
-          uint32_t *rows = rowidx + (t & 1) * 128;
-          if (p < KT) {
-            const int key = w.q.lo + tile * KT + p;
-            uint32_t row = 0xffffffffu;
-            if (key < w.q.n) {
-              const int lp = key / a.page_size;
-              const int page = __ldg(table + lp);
-              if (page >= 0 && page < a.num_pages)
-                row = (uint32_t)(((size_t)page * a.Hkv + w.kvh) * a.page_size + (key - lp * a.page_size));
-              else
-                raise_status(MOE_DEV_BAD_INDEX);
-            }
-            rows[p] = row;
-            const uint32_t m = __ballot_sync(FULL, row != 0xffffffffu);
-            if (lane == 0) masks[(t % ATTN_MASKS) * 4 + p / 32] = m;
-          }
-          ok = producers_all(ok);
-          if (!ok) {
-            leave = true;
-            break;
-          }
-          load(a.k_cache, rows);
-          if (tile == w.t0) {                          // the segment's queries
-            if (seg) ok = attn_wait(q_empty, (seg + 1) & 1, abort_flag);
-            if (ok) {
-              const uint32_t dst = smem_u32(s_q);
+      while (ok && w.next(a, units)) {
+        if (!is_k) {                                   // the segment's queries
+          if (seg) ok = __all_sync(FULL, attn_wait(q_empty, (seg + 1) & 1, abort_flag));
+          if (!ok) break;
+          const uint32_t dst = smem_u32(s_q);
 #pragma unroll 4
-              for (int r = r0; r < ATTN_ROWS; r += RPP) {
-                const int row = w.rb * ATTN_ROWS + r;
-                const bool live = row < a.rows;
-                const int tok = live ? row / group : 0, h = live ? row - tok * group : 0;
-                cp_async16_zfill(dst + place(r, ATTN_ROWS),
-                                 a.q + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + h) * D + u * 8,
-                                 live);
-              }
-              cp_async_arrive_noinc(q_full);
-              if (lane == 0) mbar_arrive(q_full);
-            }
-            ++seg;
+          for (int r = r0; r < ATTN_ROWS; r += RPP) {
+            const int row = w.rb * ATTN_ROWS + r % C::RG;       // (each lane group: all rows)
+            const bool live = row < a.rows;
+            const int tok = live ? row / group : 0, h = live ? row - tok * group : 0;
+            cp_async16_zfill(dst + place(r, ATTN_ROWS),
+                             a.q + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + h) * D + u * 8,
+                             live);
           }
-          ok = ok && slot_free();
-          if (ok) load(a.v_cache, rows);
+          cp_async_arrive_noinc(q_full);
+          if (lane == 0) mbar_arrive(q_full);
+          ++seg;
+        }
+        int next_page = a.use_tma ? page_of(w, w.q.start + w.t0 * a.tile_keys) : -1;
+        for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
+          const int k0 = w.q.start + tile * a.tile_keys;
+          const int page = next_page;
+          if (a.use_tma && tile + 1 < w.t1) next_page = page_of(w, k0 + a.tile_keys);
+          const uint32_t i = 2 * t + (is_k ? 0 : 1);   // ring index
+          uint64_t *const bar = full + i % C::kSlots;
+          const uint32_t dst = ring + (i % C::kSlots) * C::kSlot;
+          ok = i < (uint32_t)C::kSlots ||
+               attn_wait(empty + i % C::kSlots, (i / C::kSlots + 1) & 1, abort_flag);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          if (a.use_tma && __all_sync(FULL, lane >= boxes || (page >= 0 && page < a.num_pages))) {
+            if (is_k && lane < KT / 32)
+              masks[(t % ATTN_MASKS) * 4 + lane] = bit_range(0, a.tile_keys, lane);
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(bar, (uint32_t)a.tile_keys * D * 2);
+            __syncwarp();
+            // lane = page + boxes * column block (32 boxes at most)
+            const int pg = lane % boxes, c = lane / boxes;
+            const int id = __shfl_sync(FULL, page, pg);
+            if (c < D / 64)
+              tma_load_2d(attn_smem + (dst - smem_u32(attn_smem)) + c * KT * 128 + pg * box_rows * 128,
+                          map, c * 64, (id * a.Hkv + w.kvh) * a.page_size + k0 % a.page_size, bar, policy);
+            mbar_arrive(bar);
+          } else {
+            uint32_t idx[KT / 32];                     // rows lane + 32 c of the cache
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) {
+              const int e = c * 32 + lane, key = k0 + e;
+              idx[c] = 0xffffffffu;
+              if (e < a.tile_keys && key >= w.q.lo && key < w.q.n) {
+                const int lp = key / a.page_size;
+                const int id = __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
+                if (id >= 0 && id < a.num_pages)
+                  idx[c] = (uint32_t)(((size_t)id * a.Hkv + w.kvh) * a.page_size + (key - lp * a.page_size));
+                else
+                  raise_status(MOE_DEV_BAD_INDEX);
+              }
+              const uint32_t m = __ballot_sync(FULL, idx[c] != 0xffffffffu);
+              if (is_k && lane == 0) masks[(t % ATTN_MASKS) * 4 + c] = m;
+            }
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) {
+#pragma unroll 8
+              for (int j = 0; j < 32 / RPP; ++j) {
+                const int r = c * 32 + j * RPP + r0;
+                const uint32_t row = __shfl_sync(FULL, idx[c], j * RPP + r0);
+                const bool live = row != 0xffffffffu;
+                cp_async16_zfill(dst + place(r, KT), cache + (live ? (size_t)row * D : 0) + u * 8, live);
+              }
+            }
+            cp_async_arrive_noinc(bar);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0) issued[is_k ? 0 : 1] = t;
     } else if (warp == 4) {
       // ---------------------------------------------------------------- MMA --
       if (lane == 0) {
@@ -478,16 +558,27 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
       __syncwarp();
     } else {
       // ------------------------------------------------------------ softmax --
+      constexpr int NC = C::NC;
       const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+      const int kq = tid / C::RG;                           // lane group: keys [kq NC, +NC) of a tile
+      if (KS > 1) {                                         // weights of the other groups' keys: 0
+        uint32_t zero[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) zero[e] = 0;
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) tc_st32(lanes + C::kP + c * 32, zero);
+        tc_wait_st();
+      }
       uint32_t t = 0;
-      bool ok = true;
-      while (ok && w.next(a, units)) {
-        const int row = w.rb * ATTN_ROWS + tid;
-        const bool warp_live = w.rb * ATTN_ROWS + warp * 32 < a.rows;
+      bool leave = false;
+      while (!leave && w.next(a, units)) {
+        const int r = tid % C::RG, row = w.rb * ATTN_ROWS + r;
+        const bool warp_live = row - lane < a.rows;
         const int tok = row < a.rows ? row / group : 0;
         const int pos = w.q.n - a.N + tok;                  // this row sees keys (pos-window, pos]
         const int see_lo = a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;
+        bool ok = true;
         const uint32_t t_first = t, t_end = t + (uint32_t)(w.t1 - w.t0);
         for (; t < t_end; ++t) {
           ok = attn_wait(s_full + (t & 1), (t >> 1) & 1, abort_flag);
@@ -495,31 +586,31 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
           if (!ok) break;
           tc_fence_after();
           if (warp_live) {
-            uint32_t s[KT];
+            uint32_t s[NC];
 #pragma unroll
-            for (int c = 0; c < KT / 32; ++c)
-              tc_ld32(lanes + C::kS + (t & 1) * KT + c * 32, s + c * 32);
-            const int k0 = w.q.lo + (w.t0 + (int)(t - t_first)) * KT;
-            uint32_t vis[KT / 32];
-            bool all = k0 + KT - 1 <= w.q.n - a.N && (a.window == 0 || k0 > w.q.n - 1 - a.window);
+            for (int c = 0; c < NC / 32; ++c)
+              tc_ld32(lanes + C::kS + (t & 1) * KT + kq * NC + c * 32, s + c * 32);
+            const int k0 = w.q.start + (w.t0 + (int)(t - t_first)) * a.tile_keys + kq * NC;
+            uint32_t vis[NC / 32];
+            bool all = k0 + NC - 1 <= w.q.n - a.N && (a.window == 0 || k0 > w.q.n - 1 - a.window);
 #pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-              vis[c] = masks[(t % ATTN_MASKS) * 4 + c];
+            for (int c = 0; c < NC / 32; ++c) {
+              vis[c] = masks[(t % ATTN_MASKS) * 4 + kq * (NC / 32) + c];
               all = all && vis[c] == 0xffffffffu;
             }
             tc_wait_ld();
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (!all) {
 #pragma unroll
-              for (int c = 0; c < KT / 32; ++c) {
+              for (int c = 0; c < NC / 32; ++c) {
                 vis[c] &= bit_range(see_lo - k0, pos + 1 - k0, c);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if (!((vis[c] >> e) & 1)) s[c * 32 + e] = 0xff800000u;      // -infinity
               }
             }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < KT; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+            for (int e = 0; e < NC; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
             const float top =
                 fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             // raise the maximum only where a weight would pass 2^8
@@ -548,7 +639,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
             const float base = m == -INFINITY ? 0.f : m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < KT; e += 2) {
+            for (int e = 0; e < NC; e += 2) {
               const float p0 = exp2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -base));
               const float p1 = exp2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -base));
               sum[(e >> 1) & 3] += p0 + p1;
@@ -561,54 +652,98 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
               if (!ok) break;
               tc_fence_after();
             }
+            const uint32_t pt = lanes + C::kP + (t & 1) * (KT / 2) + kq * (NC / 2);
+            if constexpr (NC == 32) {
+              tc_st16(pt, s);
+            } else {
 #pragma unroll
-            for (int c = 0; c < KT / 64; ++c)
-              tc_st32(lanes + C::kP + (t & 1) * (KT / 2) + c * 32, s + c * 32);
+              for (int c = 0; c < NC / 64; ++c) tc_st32(pt + c * 32, s + c * 32);
+            }
             tc_wait_st();
           }
           tc_fence_before();
           mbar_arrive(p_full + (t & 1));
         }
-        if (!ok) break;
         // ---- the segment's end: O / l to out, or O, m, l to the workspace ----
-        ok = attn_wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
-        ok = __all_sync(FULL, ok);
-        if (!ok) break;
+        if (ok) {
+          ok = attn_wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+          ok = __all_sync(FULL, ok);
+        }
+        if (KS > 1) ok = softmax_all(ok);
+        if (!ok) {
+          leave = true;
+          break;
+        }
         tc_fence_after();
-        if (warp_live) {
-          const bool whole = w.t0 == 0 && w.t1 == w.q.tiles;
-          const bool live = row < a.rows;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
-          uint16_t *dst = a.out + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + (row - tok * group)) * D;
-          float4 *part = a.part_o + ((size_t)slot * (D / 4)) * a.rows_cap + tid;
-          if (!whole && live) a.part_ml[(size_t)slot * a.rows_cap + tid] = make_float2(m, l);
+        const bool whole = w.t0 == 0 && w.t1 == w.q.tiles, live = row < a.rows;
+        const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        uint16_t *const dst =
+            a.out + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + (row - tok * group)) * D;
+        float4 *const part = a.part_o + ((size_t)slot * (D / 4)) * a.rows_cap + r;
+        float2 *const part_ml = a.part_ml + (size_t)slot * a.rows_cap + r;
+        if constexpr (KS == 1) {
+          if (warp_live) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;      // l = 0: no key seen, O sums zeros
+            if (!whole && live) *part_ml = make_float2(m, l);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc_ld32(lanes + C::kO + c * 32, o);
-            tc_wait_ld();
-            if (!live) continue;
-            if (whole) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  // l = 0: the row saw no key (its O is a sum of zeros)
-                  const float lo = __uint_as_float(o[e + 2 * k]) * inv;
-                  const float hi = __uint_as_float(o[e + 2 * k + 1]) * inv;
-                  x[k] = cvt_bf16x2(lo, hi);
-                }
-                *reinterpret_cast<uint4 *>(dst + c * 32 + e) = make_uint4(x[0], x[1], x[2], x[3]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                part[(size_t)(c * 8 + e / 4) * a.rows_cap] =
-                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc_ld32(lanes + C::kO + c * 32, o);
+              tc_wait_ld();
+              if (!live) continue;
+              const float f = whole ? inv : 1.f;
+              attn_store<8>(whole, dst + c * 32, part + (size_t)(c * 8) * a.rows_cap, a.rows_cap,
+                            [&](int e) {
+                              return make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                                 __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+                            });
             }
+          }
+        } else {
+          // the lane groups' shares of a row meet in shared memory, 64 dims at a
+          // time: group kq adds up dims [kq 64/KS, +64/KS)
+          float2 *const ml = reinterpret_cast<float2 *>(scratch);
+          ml[tid] = make_float2(m, l);
+          softmax_sync();
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < KS; ++g) top = fmaxf(top, ml[g * C::RG + r].x);
+          const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+          for (int g = 0; g < KS; ++g) {
+            const float2 x = ml[g * C::RG + r];
+            sum += exp2_approx(x.x - base) * x.y;
+          }
+          const float f = exp2_approx(m - base) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+          if (!whole && live && kq == 0) *part_ml = make_float2(top, sum);
+          softmax_sync();
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[32];
+              tc_ld32(lanes + C::kO + c * 64 + h * 32, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                scratch[(h * 8 + e) * 128 + tid] =
+                    make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+            }
+            softmax_sync();
+            if (live)
+              attn_store<16 / KS>(whole, dst + c * 64 + kq * (64 / KS),
+                                  part + (size_t)(c * 16 + kq * (16 / KS)) * a.rows_cap, a.rows_cap,
+                                  [&](int e) {
+                                    float4 x = scratch[(kq * (16 / KS) + e) * 128 + r];
+#pragma unroll
+                                    for (int g = 1; g < KS; ++g) {
+                                      const float4 y = scratch[(kq * (16 / KS) + e) * 128 + g * C::RG + r];
+                                      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                                    }
+                                    return x;
+                                  });
+            softmax_sync();
           }
         }
         tc_fence_before();
@@ -617,6 +752,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
   }
   tc_fence_before();
   __syncthreads();
+  // after a wait that ran out: the copies still in flight into this CTA's memory
+  if (*abort_flag && tid < C::kSlots) {
+    for (int v = 0; v < 2; ++v) {                       // the slot's last K and last V tile
+      int last = -1;
+      for (int t = 0; t < (int)issued[v]; ++t)
+        if ((2 * t + v) % C::kSlots == tid) last = 2 * t + v;
+      // (a later tile of the other kind in the slot means that this one landed)
+      int other = -1;
+      for (int t = 0; t < (int)issued[1 - v]; ++t)
+        if ((2 * t + 1 - v) % C::kSlots == tid) other = 2 * t + 1 - v;
+      if (last > other) mbar_wait_drain(full + tid, (uint32_t)(last / C::kSlots) & 1);
+    }
+  }
+  __syncthreads();
   if (warp == 4) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -624,43 +773,74 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) attn_kernel(const AttnArgs a)
   }
 }
 
-// Adds the pieces of each cut item.  grid (pieces, row groups); a thread
-// owns four dims of one row.
-constexpr int JOIN_THREADS = 256;
+// Adds the pieces of each cut item in their order.  grid (pieces, row pairs in
+// strides of gridDim.y); a thread owns four dims of a row and every GROUPS-th
+// piece, the groups' sums meet in shared memory.
+constexpr int JOIN_THREADS = 512;
+constexpr int JOIN_ROWS = 2;
 
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int RPB = JOIN_THREADS / (D / 4);            // rows of a CTA
+  constexpr int UNITS = JOIN_ROWS * D / 4, GROUPS = JOIN_THREADS / UNITS;
+  __shared__ float wgt[JOIN_ROWS][ATTN_MAX_CTAS];
+  __shared__ float4 acc[GROUPS][UNITS];
   const AttnSplit sp = a.split[blockIdx.x];
   if (sp.count == 0) return;
-  const int r = blockIdx.y * RPB + threadIdx.x % RPB, d4 = threadIdx.x / RPB;
-  const int row = sp.rb * ATTN_ROWS + r;
-  if (r >= a.rows_cap || row >= a.rows) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = tid % UNITS, grp = tid / UNITS, rr = unit % JOIN_ROWS, d4 = unit / JOIN_ROWS;
+  const int group = a.Hq / a.Hkv;
   auto slot = [&](int i) { return 2 * (size_t)(sp.first + i) + (i == 0 ? 1 : 0); };
-  float m = -INFINITY;
-  for (int i = 0; i < sp.count; ++i) m = fmaxf(m, a.part_ml[slot(i) * a.rows_cap + r].x);
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (m > -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < sp.count; ++i) {
-      const float2 ml = a.part_ml[slot(i) * a.rows_cap + r];
-      const float4 x = a.part_o[(slot(i) * (D / 4) + d4) * a.rows_cap + r];
-      const float f = exp2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      o[0] = fmaf(x.x, f, o[0]);
-      o[1] = fmaf(x.y, f, o[1]);
-      o[2] = fmaf(x.z, f, o[2]);
-      o[3] = fmaf(x.w, f, o[3]);
+  const int rows = min(a.rows_cap, a.rows - sp.rb * ATTN_ROWS);
+  for (int r0 = blockIdx.y * JOIN_ROWS; r0 < rows; r0 += gridDim.y * JOIN_ROWS) {
+    // the pieces' weights 2^(m_i - m) / l: a warp per row
+    if (warp < JOIN_ROWS && r0 + warp < rows) {
+      const float2 *ml = a.part_ml + r0 + warp;
+      float m = -INFINITY, l = 0.f;
+      for (int i = lane; i < sp.count; i += 32) m = fmaxf(m, ml[slot(i) * a.rows_cap].x);
+      m = warp_max(m);
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int i = lane; i < sp.count; i += 32) {
+        const float2 x = ml[slot(i) * a.rows_cap];
+        const float f = exp2_approx(x.x - base);
+        wgt[warp][i] = f;
+        l = fmaf(x.y, f, l);
+      }
+      l = warp_sum(l);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __syncwarp();
+      for (int i = lane; i < sp.count; i += 32) wgt[warp][i] *= inv;
     }
+    __syncthreads();
+    const int r = r0 + rr;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+#pragma unroll 4
+      for (int i = grp; i < sp.count; i += GROUPS) {
+        const float4 x = a.part_o[(slot(i) * (D / 4) + d4) * a.rows_cap + r];
+        const float f = wgt[rr][i];
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      }
+    }
+    acc[grp][unit] = o;
+    __syncthreads();
+    if (grp == 0 && r < rows) {
+#pragma unroll
+      for (int g = 1; g < GROUPS; ++g) {
+        const float4 x = acc[g][unit];
+        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+      }
+      const int row = sp.rb * ATTN_ROWS + r, tok = row / group;
+      uint16_t *dst = a.out +
+                      (((size_t)sp.s * a.N + tok) * a.Hq + sp.kvh * group + (row - tok * group)) * D + d4 * 4;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+    }
+    __syncthreads();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int group = a.Hq / a.Hkv, tok = row / group;
-  uint16_t *dst =
-      a.out + (((size_t)sp.s * a.N + tok) * a.Hq + sp.kvh * group + (row - tok * group)) * D + d4 * 4;
-  *reinterpret_cast<uint2 *>(dst) =
-      make_uint2(cvt_bf16x2(o[0] * inv, o[1] * inv), cvt_bf16x2(o[2] * inv, o[3] * inv));
 }
 
 // ----------------------------------------------------------------- host --
@@ -681,9 +861,9 @@ inline AttnWs attn_ws(int N, int Hq, int Hkv, int D) {
   return w;
 }
 
-template <int D>
+template <int D, int KS>
 inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
-  typedef AttnCfg<D> C;
+  typedef AttnCfg<D, KS> C;
   static std::mutex mu;
   static uint64_t done = 0;
   int dev = 0;
@@ -692,7 +872,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!((done >> dev) & 1ull)) {
-      if (cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(attn_kernel<D, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::kSmem) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
@@ -701,25 +881,50 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
     }
   }
   const AttnWs w = attn_ws(a.N, a.Hq, a.Hkv, D);
-  a.rows = a.N * (a.Hq / a.Hkv);
   a.rows_cap = attn_rows_cap(a.N, a.Hq, a.Hkv);
   a.row_blocks = (a.rows + ATTN_ROWS - 1) / ATTN_ROWS;
   a.part_o = reinterpret_cast<float4 *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
   a.split = reinterpret_cast<AttnSplit *>(ws + w.split);
   const unsigned grid = (unsigned)std::min(sms, ATTN_MAX_CTAS);
-  cudaError_t e = launch_pdl(attn_kernel<D>, grid, ATTN_THREADS, C::kSmem, s, a);
-  if (e == cudaSuccess) {
-    constexpr int RPB = JOIN_THREADS / (D / 4);
-    e = launch_pdl(attn_join_kernel<D>, dim3(grid, (unsigned)((a.rows_cap + RPB - 1) / RPB)),
-                   JOIN_THREADS, 0, s, a);
+  // Pages of 8 rows or a multiple go by TMA (the swizzle repeats every 8 rows),
+  // as many whole ones to a tile as fit, or a tile's worth of a larger one.
+  const int ps = a.page_size;
+  CUtensorMap k_map{}, v_map{};
+  a.tile_keys = C::KT;
+  a.align = 1;
+  a.use_tma = 0;
+  if (ps % 8 == 0 && (ps <= C::KT || ps % C::KT == 0)) {
+    a.tile_keys = ps <= C::KT ? C::KT / ps * ps : C::KT;
+    a.align = std::min(ps, C::KT);
+    a.use_tma = 1;
+    const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * ps;
+    const uint32_t box = (uint32_t)a.align;
+    if (rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!make_map(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, D, rows, D * 2, 64, box) ||
+        !make_map(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v_cache, D, rows, D * 2, 64, box))
+      return MOE_ERR_CUDA;
   }
+  cudaError_t e = launch_pdl(attn_kernel<D, KS>, grid, ATTN_THREADS, C::kSmem, s, k_map, v_map, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(attn_join_kernel<D>,
+                   dim3(grid, (unsigned)std::min(8, (a.rows_cap + JOIN_ROWS - 1) / JOIN_ROWS)),
+                   JOIN_THREADS, 0, s, a);
   if (e != cudaSuccess) {
     fprintf(stderr, "mxfp4_moe: launch failed: %s\n", cudaGetErrorString(e));
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+// Lane groups by the rows to a key/value head (see the kernel's head).
+template <int D>
+inline int attn_dispatch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
+  a.rows = a.N * (a.Hq / a.Hkv);
+  return a.rows <= 32   ? attn_launch<D, D == 256 ? 2 : 4>(a, ws, sms, s)
+         : a.rows <= 64 ? attn_launch<D, 2>(a, ws, sms, s)
+                        : attn_launch<D, 1>(a, ws, sms, s);
 }
 
 }  // namespace moe

@@ -546,9 +546,9 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
   a.out = out;
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   const cudaStream_t cs = (cudaStream_t)stream;
-  return D == 64    ? attn_launch<64>(a, ws, dev->sms, cs)
-         : D == 128 ? attn_launch<128>(a, ws, dev->sms, cs)
-                    : attn_launch<256>(a, ws, dev->sms, cs);
+  return D == 64    ? attn_dispatch<64>(a, ws, dev->sms, cs)
+         : D == 128 ? attn_dispatch<128>(a, ws, dev->sms, cs)
+                    : attn_dispatch<256>(a, ws, dev->sms, cs);
 }
 
 // --------------------------------------------------------------- sampling --
