@@ -23,10 +23,11 @@
 // its unnormalised O, m and l in the workspace and attn_join_kernel adds them
 // in the order of the pieces (the same bits on every run).
 //
-// Warps: 0-3 softmax (a thread per row, tensor-memory lane = row), 4 the MMA
-// issuer, 5-8 producers: cp.async of 16-byte units, page by page, into a ring
-// of K and V tiles in the 128-byte swizzle; rows outside the sequence or on a
-// bad page are zero-filled and masked by a bit per key.
+// Warps: 0-3 softmax (a thread per row, tensor-memory lane = row; they also
+// bring the queries), 4 the MMA issuer, 5 and 6 the producers of the K and the V
+// tiles of a shared ring in the 128-byte swizzle: by TMA page by page, or row by
+// row through cp.async, where rows outside the sequence or on a bad page are
+// zero-filled and masked by a bit per key.
 //
 // Few rows would leave most lanes, and so most softmax warps, without work: up
 // to 32 rows (64) the queries stand in the 128 MMA rows four (two) times, lane
@@ -200,6 +201,11 @@ __device__ __forceinline__ void attn_store(bool whole, uint16_t *dst, float4 *pa
   }
 }
 
+// 16-byte unit u of row r in a tile of `rows` rows: blocks of 64 dims, swizzled
+__device__ __forceinline__ uint32_t attn_place(int u, int r, int rows) {
+  return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
 // Visible keys of a sequence: [lo, n), in tiles from `start` on; none for a
 // slot not in use or (reported) a length past the table's row.
 struct AttnSeq {
@@ -217,6 +223,10 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int s) {
   return AttnSeq{lo, start, n, (n - start + a.tile_keys - 1) / a.tile_keys};
 }
 
+__device__ __forceinline__ unsigned long long attn_div(unsigned long long a, unsigned long long b) {
+  return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
+}
+
 // A CTA's piece of the line of tiles, item by item.  Every role walks it alone.
 struct AttnWalk {
   unsigned long long base, pos, end;   // first tile of sequence s, next tile, end of the piece
@@ -232,7 +242,7 @@ struct AttnWalk {
       q = attn_seq(a, ++s);
     }
     const unsigned long long at = pos - base;
-    const unsigned item = (unsigned)(at / (unsigned)q.tiles);
+    const unsigned item = (unsigned)attn_div(at, (unsigned)q.tiles);
     t0 = (int)(at - (unsigned long long)item * (unsigned)q.tiles);
     t1 = (int)min((unsigned long long)q.tiles, t0 + (end - pos));
     kvh = (int)(item / (unsigned)a.row_blocks);
@@ -283,8 +293,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   uint64_t *const p_full = s_full + 2;                                         // [2]
   uint64_t *const pv_done = p_full + 2;                                        // [2]
   uint64_t *const q_full = pv_done + 2;
-  uint64_t *const q_empty = q_full + 1;
-  uint64_t *const drain = q_empty + 1;
+  uint64_t *const drain = q_full + 1;
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(drain + 1);
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drain + 1) + 1;
   int *const s_start = reinterpret_cast<int *>(drain + 2);                     // first sequence
@@ -303,8 +312,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       mbar_init(p_full + i, 128);
       mbar_init(pv_done + i, 1);
     }
-    mbar_init(q_full, 33);
-    mbar_init(q_empty, 1);
+    mbar_init(q_full, 128);
     mbar_init(drain, 1);
     *abort_flag = 0;
     issued[0] = issued[1] = 0;
@@ -344,7 +352,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     total += v;
   }
   total *= units;
-  const u64 chunk = (total + gridDim.x - 1) / gridDim.x;
+  const u64 chunk = attn_div(total + gridDim.x - 1, gridDim.x);
   const u64 start = min(total, chunk * blockIdx.x), stop = min(total, start + chunk);
   if (start < stop && before * units <= start && start < (before + mine) * units) {
     int s = q0;
@@ -359,12 +367,12 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     *s_base = base;
     // the item that this piece's start cuts, if no earlier start does
     const unsigned T = (unsigned)attn_seq(a, s).tiles;
-    const unsigned item = (unsigned)((start - base) / T);
+    const unsigned item = (unsigned)attn_div(start - base, T);
     const u64 from = base + (u64)item * T;
     AttnSplit sp{s, (int)(item / (unsigned)a.row_blocks), (int)(item % (unsigned)a.row_blocks),
-                 (int)(from / chunk), 0};
+                 (int)attn_div(from, chunk), 0};
     if (from < start && sp.first + 1 == (int)blockIdx.x)
-      sp.count = (int)((from + T - 1) / chunk) - sp.first + 1;
+      sp.count = (int)attn_div(from + T - 1, chunk) - sp.first + 1;
     a.split[blockIdx.x] = sp;
   }
   if (tid == 0 && start >= stop) a.split[blockIdx.x] = AttnSplit{0, 0, 0, 0, 0};
@@ -393,7 +401,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     const int group = a.Hq / a.Hkv;
 
     if (warp >= 5) {
-      // ------------------------------------------ producers: K and (Q, then) V --
+      // ----------------------------------------------------- producers: K and V --
       // A full tile of whole pages is a TMA box per page and 64 dims; a tile with
       // keys outside [lo, n) or on a bad page, and pages that are no whole
       // number of eight rows, go row by row through cp.async, which zero-fills
@@ -406,10 +414,6 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       const uint16_t *const cache = is_k ? a.k_cache : a.v_cache;
       const CUtensorMap *const map = is_k ? &k_map : &v_map;
       const uint64_t policy = policy_evict_normal();
-      // unit u of row r in a tile of `rows` rows: 64-dim column blocks, swizzled
-      auto place = [&](int r, int rows) -> uint32_t {
-        return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
-      };
       const int boxes = a.use_tma ? max(1, a.tile_keys / a.page_size) : 0;   // pages of a tile
       const int box_rows = a.use_tma ? a.tile_keys / boxes : 0;
       // this lane's page of the tile whose first key is k0 (whole tiles only)
@@ -418,26 +422,9 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         if (lane >= boxes || k0 < w.q.lo || k0 + a.tile_keys > w.q.n) return -1;
         return __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
       };
-      uint32_t t = 0, seg = 0;                         // tile, segment
+      uint32_t t = 0;                                  // tile
       bool ok = true;
       while (ok && w.next(a, units)) {
-        if (!is_k) {                                   // the segment's queries
-          if (seg) ok = __all_sync(FULL, attn_wait(q_empty, (seg + 1) & 1, abort_flag));
-          if (!ok) break;
-          const uint32_t dst = smem_u32(s_q);
-#pragma unroll 4
-          for (int r = r0; r < ATTN_ROWS; r += RPP) {
-            const int row = w.rb * ATTN_ROWS + r % C::RG;       // (each lane group: all rows)
-            const bool live = row < a.rows;
-            const int tok = live ? row / group : 0, h = live ? row - tok * group : 0;
-            cp_async16_zfill(dst + place(r, ATTN_ROWS),
-                             a.q + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + h) * D + u * 8,
-                             live);
-          }
-          cp_async_arrive_noinc(q_full);
-          if (lane == 0) mbar_arrive(q_full);
-          ++seg;
-        }
         int next_page = a.use_tma ? page_of(w, w.q.start + w.t0 * a.tile_keys) : -1;
         for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
           const int k0 = w.q.start + tile * a.tile_keys;
@@ -487,7 +474,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 const int r = c * 32 + j * RPP + r0;
                 const uint32_t row = __shfl_sync(FULL, idx[c], j * RPP + r0);
                 const bool live = row != 0xffffffffu;
-                cp_async16_zfill(dst + place(r, KT), cache + (live ? (size_t)row * D : 0) + u * 8, live);
+                cp_async16_zfill(dst + attn_place(u, r, KT), cache + (live ? (size_t)row * D : 0) + u * 8, live);
               }
             }
             cp_async_arrive_noinc(bar);
@@ -530,11 +517,9 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         while (ok && w.next(a, units)) {
           const uint32_t t_end = t + (uint32_t)(w.t1 - w.t0), t_first = t;
           ok = attn_wait(q_full, seg & 1, abort_flag) && scores(t);
-          if (ok && t + 1 == t_end) tc_commit(q_empty);
           for (; ok && t < t_end; ++t) {
             if (t + 1 < t_end) {
               ok = scores(t + 1);
-              if (ok && t + 2 == t_end) tc_commit(q_empty);
             }
             ok = ok && attn_wait(p_full + (t & 1), (t >> 1) & 1, abort_flag);
             if (!ok) break;
@@ -570,9 +555,32 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         tc_wait_st();
       }
       uint32_t t = 0;
-      bool leave = false;
-      while (!leave && w.next(a, units)) {
-        const int r = tid % C::RG, row = w.rb * ATTN_ROWS + r;
+      const int r = tid % C::RG;
+      // A segment's queries, each warp the rows of its lanes (rows past the last
+      // are left as they are: they reach no output).  Called once all score MMAs
+      // of the segment before are complete.
+      auto load_q = [&](const AttnWalk &g) {
+        constexpr int UNITS = D / 8, RPP = 32 / UNITS;
+        const int row = g.rb * ATTN_ROWS + r;
+        if (row - lane < a.rows) {
+          const uint16_t *src = a.q + (size_t)g.s * a.N * a.Hq * D;
+          const int u = lane % UNITS, r0 = lane / UNITS, tok = row / group;
+          const int at = row < a.rows ? (tok * a.Hq + g.kvh * group + row - tok * group) * D : -1;
+          const uint32_t dst = smem_u32(s_q);
+#pragma unroll 8
+          for (int j = 0; j < 32 / RPP; ++j) {
+            const int from = __shfl_sync(FULL, at, j * RPP + r0);
+            if (from >= 0)
+              cp_async16_zfill(dst + attn_place(u, warp * 32 + j * RPP + r0, ATTN_ROWS),
+                               src + from + u * 8, true);
+          }
+        }
+        cp_async_arrive_noinc(q_full);
+      };
+      bool more = w.next(a, units);
+      if (more) load_q(w);
+      while (more) {
+        const int row = w.rb * ATTN_ROWS + r;
         const bool warp_live = row - lane < a.rows;
         const int tok = row < a.rows ? row / group : 0;
         const int pos = w.q.n - a.N + tok;                  // this row sees keys (pos-window, pos]
@@ -664,16 +672,17 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           tc_fence_before();
           mbar_arrive(p_full + (t & 1));
         }
-        // ---- the segment's end: O / l to out, or O, m, l to the workspace ----
+        // ---- the segment's end: O / l to out, or O, m, l to the workspace; the
+        // next segment's queries on their way ----
+        AttnWalk ahead = w;
+        more = ahead.next(a, units);
         if (ok) {
+          if (more) load_q(ahead);
           ok = attn_wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
           ok = __all_sync(FULL, ok);
         }
         if (KS > 1) ok = softmax_all(ok);
-        if (!ok) {
-          leave = true;
-          break;
-        }
+        if (!ok) break;
         tc_fence_after();
         const bool whole = w.t0 == 0 && w.t1 == w.q.tiles, live = row < a.rows;
         const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
@@ -747,7 +756,9 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           }
         }
         tc_fence_before();
+        w = ahead;
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   tc_fence_before();
