@@ -56,7 +56,7 @@ struct AttnArgs {
   float scale_log2;                    // scale * log2(e), > 0
   int window;
   uint16_t *out;                       // [S, N, Hq, D]
-  // workspace: unnormalised O [2G][D/4][rows_cap] float4, (m, l) [2G][rows_cap],
+  // workspace: unnormalised O [2G][rows_cap][D/4] float4, (m, l) [2G][rows_cap],
   // one AttnSplit per piece
   // keys of a tile, and what its first key is a multiple of: whole pages where
   // the pages go by TMA (use_tma), else KT and 1
@@ -80,8 +80,11 @@ struct AttnCfg {
   static constexpr int RG = ATTN_ROWS / KS;           // rows of a lane group
   static constexpr int kSlot = KT * D * 2;            // one K or V tile
   static constexpr int kQ = ATTN_ROWS * D * 2;
-  static constexpr int kScratch = KS > 1 ? 32768 : 0; // 64 dims of O for the groups' sum
-  static constexpr int kSlots = (D == 64 ? 12 : D == 128 ? 6 : 5) - kScratch / kSlot;
+  // 64 dims of O for the groups' sum: 16 columns of 128 float4, one apart more so
+  // that the 16 quads of a row lie in different banks
+  static constexpr int kScratchPitch = 129;
+  static constexpr int kScratch = KS > 1 ? 16 * kScratchPitch * 16 : 0;
+  static constexpr int kSlots = (D == 64 ? 12 : D == 128 ? 6 : 5) - (KS > 1 ? 32768 / kSlot : 0);
   static constexpr int kMisc = 2048;
   static constexpr int kSmem = kQ + kSlots * kSlot + kScratch + kMisc;
   // tensor memory columns: S x2, O, P x2 (two bf16 to a column)
@@ -184,23 +187,6 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
-// 4 COUNT dims of a row, value(i) the i-th four: to out as bf16, or to a piece
-template <int COUNT, typename F>
-__device__ __forceinline__ void attn_store(bool whole, uint16_t *dst, float4 *part, int stride,
-                                           F value) {
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < COUNT; i += 2) {
-      const float4 x = value(i), y = value(i + 1);
-      *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(
-          cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w), cvt_bf16x2(y.x, y.y), cvt_bf16x2(y.z, y.w));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) part[(size_t)i * stride] = value(i);
-  }
-}
-
 // 16-byte unit u of row r in a tile of `rows` rows: blocks of 64 dims, swizzled
 __device__ __forceinline__ uint32_t attn_place(int u, int r, int rows) {
   return (uint32_t)((u >> 3) * rows * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4));
@@ -287,7 +273,8 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   float4 *const scratch = reinterpret_cast<float4 *>(s_ring + C::kSlots * C::kSlot);
   uint8_t *const misc = s_ring + C::kSlots * C::kSlot + C::kScratch;
   uint32_t *const masks = reinterpret_cast<uint32_t *>(misc);                  // [8][4]
-  uint64_t *const full = reinterpret_cast<uint64_t *>(masks + ATTN_MASKS * 4); // [kSlots]
+  int *const row_at = reinterpret_cast<int *>(masks + ATTN_MASKS * 4);         // [64]
+  uint64_t *const full = reinterpret_cast<uint64_t *>(row_at + 64);            // [kSlots]
   uint64_t *const empty = full + C::kSlots;                                    // [kSlots]
   uint64_t *const s_full = empty + C::kSlots;                                  // [2]
   uint64_t *const p_full = s_full + 2;                                         // [2]
@@ -365,24 +352,26 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     }
     *s_start = s;
     *s_base = base;
-    // the item that this piece's start cuts, if no earlier start does
-    const unsigned T = (unsigned)attn_seq(a, s).tiles;
-    const unsigned item = (unsigned)attn_div(start - base, T);
-    const u64 from = base + (u64)item * T;
-    AttnSplit sp{s, (int)(item / (unsigned)a.row_blocks), (int)(item % (unsigned)a.row_blocks),
-                 (int)attn_div(from, chunk), 0};
-    if (from < start && sp.first + 1 == (int)blockIdx.x)
-      sp.count = (int)attn_div(from + T - 1, chunk) - sp.first + 1;
-    a.split[blockIdx.x] = sp;
-  }
-  if (tid == 0 && start >= stop) a.split[blockIdx.x] = AttnSplit{0, 0, 0, 0, 0};
-  // sequences without a key: zeros
-  for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
-    if (attn_seq(a, s).tiles) continue;
-    uint4 *o = reinterpret_cast<uint4 *>(a.out + (size_t)s * a.N * a.Hq * D);
-    for (int i = tid; i < a.N * a.Hq * (D / 8); i += ATTN_THREADS) o[i] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
+  // What the softmax warps do beside: sequences without a key get zeros, and
+  // the item that this piece's start cuts, if no earlier start does, is noted.
+  auto beside = [&](const AttnWalk *w) {
+    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+      if (attn_seq(a, s).tiles) continue;
+      uint4 *o = reinterpret_cast<uint4 *>(a.out + (size_t)s * a.N * a.Hq * D);
+      for (int i = tid; i < a.N * a.Hq * (D / 8); i += 128) o[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (tid == 0) {
+      AttnSplit sp{0, 0, 0, 0, 0};
+      if (w != nullptr && w->t0 > 0) {           // (w: the piece's first segment)
+        const u64 from = start - (unsigned)w->t0, to = from + (unsigned)w->q.tiles - 1;
+        sp = AttnSplit{w->s, w->kvh, w->rb, (int)attn_div(from, chunk), 0};
+        if (sp.first + 1 == (int)blockIdx.x) sp.count = (int)attn_div(to, chunk) - sp.first + 1;
+      }
+      a.split[blockIdx.x] = sp;
+    }
+  };
 
   if (start < stop) {
     AttnWalk w;
@@ -579,6 +568,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       };
       bool more = w.next(a, units);
       if (more) load_q(w);
+      beside(&w);
       while (more) {
         const int row = w.rb * ATTN_ROWS + r;
         const bool warp_live = row - lane < a.rows;
@@ -688,12 +678,11 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
         uint16_t *const dst =
             a.out + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + (row - tok * group)) * D;
-        float4 *const part = a.part_o + ((size_t)slot * (D / 4)) * a.rows_cap + r;
-        float2 *const part_ml = a.part_ml + (size_t)slot * a.rows_cap + r;
+        float4 *const part = a.part_o + ((size_t)slot * a.rows_cap + r) * (D / 4);
         if constexpr (KS == 1) {
           if (warp_live) {
             const float inv = l > 0.f ? 1.f / l : 0.f;      // l = 0: no key seen, O sums zeros
-            if (!whole && live) *part_ml = make_float2(m, l);
+            if (!whole && live) a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -701,18 +690,31 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
               tc_wait_ld();
               if (!live) continue;
               const float f = whole ? inv : 1.f;
-              attn_store<8>(whole, dst + c * 32, part + (size_t)(c * 8) * a.rows_cap, a.rows_cap,
-                            [&](int e) {
-                              return make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                                 __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
-                            });
+              auto quad = [&](int e) {
+                return make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                   __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+              };
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float4 x = quad(e), y = quad(e + 1);
+                if (whole) {
+                  *reinterpret_cast<uint4 *>(dst + c * 32 + 4 * e) =
+                      make_uint4(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w), cvt_bf16x2(y.x, y.y),
+                                 cvt_bf16x2(y.z, y.w));
+                } else {
+                  part[c * 8 + e] = x;
+                  part[c * 8 + e + 1] = y;
+                }
+              }
             }
           }
         } else {
           // the lane groups' shares of a row meet in shared memory, 64 dims at a
-          // time: group kq adds up dims [kq 64/KS, +64/KS)
+          // time; 16 threads then add up and write a row's quads
+          constexpr int PITCH = C::kScratchPitch;
           float2 *const ml = reinterpret_cast<float2 *>(scratch);
           ml[tid] = make_float2(m, l);
+          if (kq == 0) row_at[r] = live ? (tok * a.Hq + row - tok * group) * D : -1;
           softmax_sync();
           float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -724,8 +726,12 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             sum += exp2_approx(x.x - base) * x.y;
           }
           const float f = exp2_approx(m - base) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
-          if (!whole && live && kq == 0) *part_ml = make_float2(top, sum);
+          if (!whole && live && kq == 0) a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(top, sum);
           softmax_sync();
+          uint16_t *const item =
+              a.out + ((size_t)w.s * a.N * a.Hq + w.kvh * group) * D + (tid & 15) * 4;
+          float4 *const piece = a.part_o + (size_t)slot * a.rows_cap * (D / 4) + (tid & 15);
+          const int rows = min(C::RG, a.rows);
 #pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
@@ -735,23 +741,25 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
               tc_wait_ld();
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                scratch[(h * 8 + e) * 128 + tid] =
+                scratch[(h * 8 + e) * PITCH + tid] =
                     make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
                                 __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
             }
             softmax_sync();
-            if (live)
-              attn_store<16 / KS>(whole, dst + c * 64 + kq * (64 / KS),
-                                  part + (size_t)(c * 16 + kq * (16 / KS)) * a.rows_cap, a.rows_cap,
-                                  [&](int e) {
-                                    float4 x = scratch[(kq * (16 / KS) + e) * 128 + r];
+            for (int rr = tid >> 4; rr < rows; rr += 8) {
+              const float4 *const from = scratch + (tid & 15) * PITCH + rr;
+              float4 x = from[0];
 #pragma unroll
-                                    for (int g = 1; g < KS; ++g) {
-                                      const float4 y = scratch[(kq * (16 / KS) + e) * 128 + g * C::RG + r];
-                                      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                                    }
-                                    return x;
-                                  });
+              for (int g = 1; g < KS; ++g) {
+                const float4 y = from[g * C::RG];
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+              }
+              if (whole)
+                *reinterpret_cast<uint2 *>(item + row_at[rr] + c * 64) =
+                    make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
+              else
+                piece[(size_t)rr * (D / 4) + c * 16] = x;
+            }
             softmax_sync();
           }
         }
@@ -760,6 +768,8 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
+  } else if (warp < 4) {
+    beside(nullptr);
   }
   tc_fence_before();
   __syncthreads();
@@ -784,68 +794,108 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   }
 }
 
-// Adds the pieces of each cut item in their order.  grid (pieces, row pairs in
-// strides of gridDim.y); a thread owns four dims of a row and every GROUPS-th
-// piece, the groups' sums meet in shared memory.
+// Adds the pieces of the cut items.  A CTA takes units of (item, a few of its
+// rows); a thread owns four dims of a row and every G-th piece, and the G
+// groups' sums meet in shared memory, always in the same order.  G grows with
+// the pieces (148 of one item where a single sequence fills the GPU, two or
+// three where many do), the rows of a unit shrink with it.
 constexpr int JOIN_THREADS = 512;
-constexpr int JOIN_ROWS = 2;
 
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs a, int pieces) {
   pdl_wait();
   pdl_trigger();
-  constexpr int UNITS = JOIN_ROWS * D / 4, GROUPS = JOIN_THREADS / UNITS;
-  __shared__ float wgt[JOIN_ROWS][ATTN_MAX_CTAS];
-  __shared__ float4 acc[GROUPS][UNITS];
-  const AttnSplit sp = a.split[blockIdx.x];
-  if (sp.count == 0) return;
+  constexpr int QUADS = D / 4;
+  constexpr int MOST_ROWS = JOIN_THREADS / QUADS;        // G = 1
+  __shared__ float wgt[16 * ATTN_MAX_CTAS];
+  __shared__ float4 acc[JOIN_THREADS];
+  __shared__ AttnSplit items[ATTN_MAX_CTAS];
+  __shared__ int first[ATTN_MAX_CTAS + 1];               // units before an item
+  __shared__ int warp_sum[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = tid % UNITS, grp = tid / UNITS, rr = unit % JOIN_ROWS, d4 = unit / JOIN_ROWS;
   const int group = a.Hq / a.Hkv;
-  auto slot = [&](int i) { return 2 * (size_t)(sp.first + i) + (i == 0 ? 1 : 0); };
-  const int rows = min(a.rows_cap, a.rows - sp.rb * ATTN_ROWS);
-  for (int r0 = blockIdx.y * JOIN_ROWS; r0 < rows; r0 += gridDim.y * JOIN_ROWS) {
+  // groups of pieces: a unit's weights (rows x pieces) fit `wgt` either way
+  auto shift_of = [](int count) { return count > 16 ? 3 : count > 4 ? 1 : 0; };
+  auto rows_of = [&](const AttnSplit &sp) { return min(ATTN_ROWS, a.rows - sp.rb * ATTN_ROWS); };
+  int mine = 0;
+  if (tid < pieces) {
+    const AttnSplit sp = a.split[tid];
+    items[tid] = sp;
+    const int rpu = MOST_ROWS >> shift_of(sp.count);
+    mine = sp.count ? (rows_of(sp) + rpu - 1) / rpu : 0;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31 && warp < 8) warp_sum[warp] = upto;
+  __syncthreads();
+  for (int i = 0; i < min(warp, 8); ++i) upto += warp_sum[i];
+  if (tid < pieces) first[tid + 1] = upto;
+  if (tid == 0) first[0] = 0;
+  __syncthreads();
+  const int total = first[pieces];
+
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int lo = 0, hi = pieces;                             // the item: first[lo] <= u < first[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const AttnSplit sp = items[lo];
+    const int sh = shift_of(sp.count), G = 1 << sh, rpu = MOST_ROWS >> sh;
+    const int r0 = (u - first[lo]) * rpu, rows = min(rpu, rows_of(sp) - r0);
+    auto slot = [&](int i) { return 2 * (size_t)(sp.first + i) + (i == 0 ? 1 : 0); };
     // the pieces' weights 2^(m_i - m) / l: a warp per row
-    if (warp < JOIN_ROWS && r0 + warp < rows) {
-      const float2 *ml = a.part_ml + r0 + warp;
+    for (int rr = warp; rr < rows; rr += JOIN_THREADS / 32) {
+      const float2 *ml = a.part_ml + r0 + rr;
+      constexpr int MOST = (ATTN_MAX_CTAS + 31) / 32;
+      float2 x[MOST];
       float m = -INFINITY, l = 0.f;
-      for (int i = lane; i < sp.count; i += 32) m = fmaxf(m, ml[slot(i) * a.rows_cap].x);
+#pragma unroll
+      for (int j = 0; j < MOST; ++j)
+        x[j] = lane + 32 * j < sp.count ? ml[slot(lane + 32 * j) * a.rows_cap] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < MOST; ++j) m = fmaxf(m, x[j].x);
       m = warp_max(m);
       const float base = m == -INFINITY ? 0.f : m;
-      for (int i = lane; i < sp.count; i += 32) {
-        const float2 x = ml[slot(i) * a.rows_cap];
-        const float f = exp2_approx(x.x - base);
-        wgt[warp][i] = f;
-        l = fmaf(x.y, f, l);
+#pragma unroll
+      for (int j = 0; j < MOST; ++j) {
+        x[j].x = exp2_approx(x[j].x - base);
+        l = fmaf(x[j].y, x[j].x, l);
       }
-      l = warp_sum(l);
+      l = moe::warp_sum(l);
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      __syncwarp();
-      for (int i = lane; i < sp.count; i += 32) wgt[warp][i] *= inv;
+#pragma unroll
+      for (int j = 0; j < MOST; ++j)
+        if (lane + 32 * j < sp.count) wgt[rr * sp.count + lane + 32 * j] = x[j].x * inv;
     }
+    const int d4 = tid % QUADS, rr = (tid / QUADS) % rpu, grp = tid / (rpu * QUADS);
     __syncthreads();
-    const int r = r0 + rr;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
+    if (rr < rows) {
+      const float4 *x0 = a.part_o + (size_t)(r0 + rr) * QUADS + d4;
 #pragma unroll 4
-      for (int i = grp; i < sp.count; i += GROUPS) {
-        const float4 x = a.part_o[(slot(i) * (D / 4) + d4) * a.rows_cap + r];
-        const float f = wgt[rr][i];
+      for (int i = grp; i < sp.count; i += G) {
+        const float4 x = x0[slot(i) * QUADS * a.rows_cap];
+        const float f = wgt[rr * sp.count + i];
         o.x = fmaf(x.x, f, o.x);
         o.y = fmaf(x.y, f, o.y);
         o.z = fmaf(x.z, f, o.z);
         o.w = fmaf(x.w, f, o.w);
       }
     }
-    acc[grp][unit] = o;
+    acc[tid] = o;
     __syncthreads();
-    if (grp == 0 && r < rows) {
-#pragma unroll
-      for (int g = 1; g < GROUPS; ++g) {
-        const float4 x = acc[g][unit];
+    if (grp == 0 && rr < rows) {
+      for (int g = 1; g < G; ++g) {
+        const float4 x = acc[tid + g * rpu * QUADS];
         o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
       }
-      const int row = sp.rb * ATTN_ROWS + r, tok = row / group;
+      const int row = sp.rb * ATTN_ROWS + r0 + rr, tok = row / group;
       uint16_t *dst = a.out +
                       (((size_t)sp.s * a.N + tok) * a.Hq + sp.kvh * group + (row - tok * group)) * D + d4 * 4;
       *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
@@ -884,7 +934,11 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
     std::lock_guard<std::mutex> lk(mu);
     if (!((done >> dev) & 1ull)) {
       if (cudaFuncSetAttribute(attn_kernel<D, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::kSmem) != cudaSuccess) {
+                               C::kSmem) != cudaSuccess ||
+          // (the join runs between two attention kernels: the same split of an
+          // SM's memory, which is changed on an idle SM only)
+          cudaFuncSetAttribute(attn_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
       }
@@ -918,9 +972,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   }
   cudaError_t e = launch_pdl(attn_kernel<D, KS>, grid, ATTN_THREADS, C::kSmem, s, k_map, v_map, a);
   if (e == cudaSuccess)
-    e = launch_pdl(attn_join_kernel<D>,
-                   dim3(grid, (unsigned)std::min(8, (a.rows_cap + JOIN_ROWS - 1) / JOIN_ROWS)),
-                   JOIN_THREADS, 0, s, a);
+    e = launch_pdl(attn_join_kernel<D>, 2 * grid, JOIN_THREADS, 0, s, a, (int)grid);
   if (e != cudaSuccess) {
     fprintf(stderr, "mxfp4_moe: launch failed: %s\n", cudaGetErrorString(e));
     cudaGetLastError();
