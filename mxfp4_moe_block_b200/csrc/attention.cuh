@@ -42,8 +42,10 @@ namespace moe {
 
 constexpr int ATTN_MAX_CTAS = 148;
 constexpr int ATTN_ROWS = 128;
-constexpr int ATTN_THREADS = 224;
 constexpr int ATTN_MASKS = 8;
+#ifndef ATTN_KS64
+#define ATTN_KS64 0
+#endif
 
 struct AttnArgs {
   const uint16_t *q;                   // [S, N, Hq, D]
@@ -75,24 +77,27 @@ struct AttnSplit {
 
 template <int D, int KS>
 struct AttnCfg {
-  static constexpr int KT = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int KT = D == 256 || (D == 128 && KS == ATTN_KS64) ? 64 : 128;   // keys per tile
+  static constexpr int WGS = D == 256 || KT == 128 && D == 128 ? 1 : 2;  // softmax warpgroups, a tile each in turn
   static constexpr int NC = KT / KS;                  // keys of a tile to one softmax thread
   static constexpr int RG = ATTN_ROWS / KS;           // rows of a lane group
+  static constexpr int kSoftmax = 128 * WGS;          // softmax threads
+  static constexpr int kThreads = kSoftmax + 96;      // and the MMA, K and V warps
   static constexpr int kSlot = KT * D * 2;            // one K or V tile
   static constexpr int kQ = ATTN_ROWS * D * 2;
-  // 64 dims of O for the groups' sum: 16 columns of 128 float4, one apart more so
-  // that the 16 quads of a row lie in different banks
-  static constexpr int kScratchPitch = 129;
-  static constexpr int kScratch = KS > 1 ? 16 * kScratchPitch * 16 : 0;
-  static constexpr int kSlots = (D == 64 ? 12 : D == 128 ? 6 : 5) - (KS > 1 ? 32768 / kSlot : 0);
+  // 32 dims of O for the groups' sum: 8 columns of a float4 per softmax thread,
+  // one apart more so that the quads of a row lie in different banks
+  static constexpr int kPitch = kSoftmax + 1;
+  static constexpr int kScratch = 8 * kPitch * 16;
   static constexpr int kMisc = 2048;
+  static constexpr int kSlots = (232448 - kQ - kScratch - kMisc) / kSlot;
   static constexpr int kSmem = kQ + kSlots * kSlot + kScratch + kMisc;
-  // tensor memory columns: S x2, O, P x2 (two bf16 to a column)
-  static constexpr uint32_t kS = 0, kO = D == 256 ? 256 : 2 * KT;
-  static constexpr uint32_t kP = D == 256 ? 2 * KT : kO + D;
+  // Tensor memory columns: S and P (two bf16 to a column) of two tiles in flight,
+  // O of each warpgroup.
+  static constexpr uint32_t kS = 0, kP = 2 * KT, kO = 512 - WGS * D;
   static constexpr uint32_t kCols = 512;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
-  static_assert(kP + KT <= kCols && kO + D <= kCols, "tensor memory");
+  static_assert(kP + KT <= kO, "tensor memory");
 };
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool live) {
@@ -101,12 +106,16 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, 
                : "memory");
 }
 
+// The MMA warp runs its loop as a whole, one elected lane issuing: addresses and
+// descriptors then stay in uniform registers (with a single lane in the loop every
+// operand was moved there anew, ~50 ns an MMA, which bound the whole kernel).
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -114,10 +123,19 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 // bf16 x bf16 -> float, M = 128; transpose_b: B is N-major in shared memory
@@ -213,28 +231,57 @@ __device__ __forceinline__ unsigned long long attn_div(unsigned long long a, uns
   return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
 }
 
+// A place in the ring and the parity of its barriers' phase.  K and V tiles share
+// the ring in the order K0 K1 V0 K2 V1 K3 .. in which they are used.
+template <int SLOTS>
+struct AttnRing {
+  uint32_t slot, phase;
+  __device__ __forceinline__ explicit AttnRing(uint32_t first) : slot(first), phase(0) {}
+  __device__ __forceinline__ void advance(uint32_t n) {
+    slot += n;
+    if (slot >= SLOTS) {
+      slot -= SLOTS;
+      phase ^= 1;
+    }
+  }
+};
+
+constexpr unsigned ATTN_ITEM_COST = 3;
+__device__ __forceinline__ unsigned attn_cost(int tiles) {
+  return tiles ? (unsigned)tiles + ATTN_ITEM_COST : 0;
+}
+
 // A CTA's piece of the line of tiles, item by item.  Every role walks it alone.
+// An item counts ATTN_ITEM_COST tiles more than it has: what its start and end
+// (queries, first tiles, O out) cost a CTA, so that CTAs with many short items
+// end with the others.
 struct AttnWalk {
   unsigned long long base, pos, end;   // first tile of sequence s, next tile, end of the piece
   AttnSeq q;
   int s;
-  // the segment: tiles [t0, t1) of an item of q.tiles tiles
+  // the segment: tiles [t0, t1) of an item of q.tiles tiles that starts at item_at
   int kvh, rb, t0, t1;
+  unsigned long long item_at;
 
   __device__ __forceinline__ bool next(const AttnArgs &a, unsigned units) {
-    if (pos >= end) return false;
-    while (pos >= base + (unsigned long long)q.tiles * units) {
-      base += (unsigned long long)q.tiles * units;
-      q = attn_seq(a, ++s);
+    for (;;) {
+      if (pos >= end) return false;
+      while (pos >= base + (unsigned long long)attn_cost(q.tiles) * units) {
+        base += (unsigned long long)attn_cost(q.tiles) * units;
+        q = attn_seq(a, ++s);
+      }
+      const unsigned cost = attn_cost(q.tiles);
+      const unsigned long long at = pos - base;
+      const unsigned item = (unsigned)attn_div(at, cost);
+      t0 = (int)(at - (unsigned long long)item * cost);
+      t1 = (int)min((unsigned long long)q.tiles, t0 + (end - pos));
+      kvh = (int)(item / (unsigned)a.row_blocks);
+      rb = (int)(item - (unsigned)kvh * (unsigned)a.row_blocks);
+      item_at = base + (unsigned long long)item * cost;
+      const bool some = t0 < q.tiles;                  // (else in the item's extra cost)
+      pos = t1 < q.tiles ? pos + (t1 - t0) : item_at + cost;
+      if (some) return true;
     }
-    const unsigned long long at = pos - base;
-    const unsigned item = (unsigned)attn_div(at, (unsigned)q.tiles);
-    t0 = (int)(at - (unsigned long long)item * (unsigned)q.tiles);
-    t1 = (int)min((unsigned long long)q.tiles, t0 + (end - pos));
-    kvh = (int)(item / (unsigned)a.row_blocks);
-    rb = (int)(item - (unsigned)kvh * (unsigned)a.row_blocks);
-    pos += t1 - t0;
-    return true;
   }
 };
 
@@ -249,23 +296,28 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b, int w) {
 
 // true iff `v` holds on every softmax thread (named barrier 1), so that they
 // decide together to stay or leave
+template <int THREADS>
 __device__ __forceinline__ bool softmax_all(bool v) {
   uint32_t r;
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"((uint32_t)v) : "memory");
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"((uint32_t)v), "n"(THREADS) : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 template <int D, int KS>
-__global__ void __launch_bounds__(ATTN_THREADS, 1)
+__global__ void __launch_bounds__(AttnCfg<D, KS>::kThreads, 1)
 attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
             const AttnArgs a) {
   typedef AttnCfg<D, KS> C;
-  constexpr int KT = C::KT;
+  constexpr int KT = C::KT, WGS = C::WGS, THREADS = C::kThreads;
+  constexpr int MMA_WARP = 4 * WGS, K_WARP = MMA_WARP + 1;
   typedef unsigned long long u64;
   extern __shared__ __align__(1024) uint8_t attn_smem[];
   uint8_t *const s_q = attn_smem;
@@ -273,12 +325,13 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   float4 *const scratch = reinterpret_cast<float4 *>(s_ring + C::kSlots * C::kSlot);
   uint8_t *const misc = s_ring + C::kSlots * C::kSlot + C::kScratch;
   uint32_t *const masks = reinterpret_cast<uint32_t *>(misc);                  // [8][4]
-  int *const row_at = reinterpret_cast<int *>(masks + ATTN_MASKS * 4);         // [64]
-  uint64_t *const full = reinterpret_cast<uint64_t *>(row_at + 64);            // [kSlots]
+  int *const row_at = reinterpret_cast<int *>(masks + ATTN_MASKS * 4);         // [128]
+  uint64_t *const full = reinterpret_cast<uint64_t *>(row_at + ATTN_ROWS);     // [kSlots]
   uint64_t *const empty = full + C::kSlots;                                    // [kSlots]
-  uint64_t *const s_full = empty + C::kSlots;                                  // [2]
-  uint64_t *const p_full = s_full + 2;                                         // [2]
-  uint64_t *const pv_done = p_full + 2;                                        // [2]
+  uint64_t *const s_full = empty + C::kSlots;                                  // [2] S written
+  uint64_t *const s_free = s_full + 2;                                         // [2] S read
+  uint64_t *const p_full = s_free + 2;                                         // [2] P written
+  uint64_t *const pv_done = p_full + 2;                                        // [2] P read, O summed
   uint64_t *const q_full = pv_done + 2;
   uint64_t *const drain = q_full + 1;
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(drain + 1);
@@ -291,21 +344,22 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, 33);
+      mbar_init(full + i, 32);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 128);
       mbar_init(p_full + i, 128);
       mbar_init(pv_done + i, 1);
     }
-    mbar_init(q_full, 128);
+    mbar_init(q_full, C::kSoftmax);
     mbar_init(drain, 1);
     *abort_flag = 0;
     issued[0] = issued[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
                  "r"(C::kCols));
@@ -316,10 +370,10 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
 
   // ---- this CTA's piece: prefix sums of the sequences' tiles ----
   const unsigned units = (unsigned)a.Hkv * (unsigned)a.row_blocks;   // items per sequence
-  const int per = (a.S + ATTN_THREADS - 1) / ATTN_THREADS;
+  const int per = (a.S + THREADS - 1) / THREADS;
   const int q0 = min(a.S, tid * per), q1 = min(a.S, q0 + per);
   u64 mine = 0;
-  for (int s = q0; s < q1; ++s) mine += attn_seq(a, s).tiles;
+  for (int s = q0; s < q1; ++s) mine += attn_cost(attn_seq(a, s).tiles);
   u64 upto = mine;                                 // inclusive prefix over the warp
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -333,7 +387,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   const uint32_t tmem = *tmem_slot;
   u64 before = upto - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i < ATTN_THREADS / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     const u64 v = scan[i];
     if (i < warp) before += v;
     total += v;
@@ -345,7 +399,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     int s = q0;
     u64 base = before * units;
     for (;;) {
-      const u64 t = (u64)attn_seq(a, s).tiles * units;
+      const u64 t = (u64)attn_cost(attn_seq(a, s).tiles) * units;
       if (start < base + t) break;
       base += t;
       ++s;
@@ -360,12 +414,12 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
       if (attn_seq(a, s).tiles) continue;
       uint4 *o = reinterpret_cast<uint4 *>(a.out + (size_t)s * a.N * a.Hq * D);
-      for (int i = tid; i < a.N * a.Hq * (D / 8); i += 128) o[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < a.N * a.Hq * (D / 8); i += C::kSoftmax) o[i] = make_uint4(0, 0, 0, 0);
     }
     if (tid == 0) {
       AttnSplit sp{0, 0, 0, 0, 0};
       if (w != nullptr && w->t0 > 0) {           // (w: the piece's first segment)
-        const u64 from = start - (unsigned)w->t0, to = from + (unsigned)w->q.tiles - 1;
+        const u64 from = w->item_at, to = from + (unsigned)w->q.tiles - 1;
         sp = AttnSplit{w->s, w->kvh, w->rb, (int)attn_div(from, chunk), 0};
         if (sp.first + 1 == (int)blockIdx.x) sp.count = (int)attn_div(to, chunk) - sp.first + 1;
       }
@@ -383,23 +437,22 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     // rows that a tile of whole pages leaves unused: their weights are 0, their
     // values must not be NaN
     if (a.tile_keys < KT)
-      for (int i = tid; i < C::kSlots * C::kSlot / 16; i += ATTN_THREADS)
+      for (int i = tid; i < C::kSlots * C::kSlot / 16; i += THREADS)
         reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
     __syncthreads();       // (the scan's memory becomes Q)
     const int group = a.Hq / a.Hkv;
 
-    if (warp >= 5) {
+    if (warp >= K_WARP) {
       // ----------------------------------------------------- producers: K and V --
       // A full tile of whole pages is a TMA box per page and 64 dims; a tile with
       // keys outside [lo, n) or on a bad page, and pages that are no whole
       // number of eight rows, go row by row through cp.async, which zero-fills
-      // what is outside.  Either way a slot's barrier gets 33 arrivals.
+      // what is outside.  Either way a slot's barrier gets an arrival a lane.
       constexpr int UNITS = D / 8;                     // 16-byte units of a row
       constexpr int RPP = 32 / UNITS;                  // rows of one pass of the warp
-      const bool is_k = warp == 5;
+      const bool is_k = warp == K_WARP;
       const int u = lane % UNITS, r0 = lane / UNITS;
-      const uint32_t ring = smem_u32(s_ring);
       const uint16_t *const cache = is_k ? a.k_cache : a.v_cache;
       const CUtensorMap *const map = is_k ? &k_map : &v_map;
       const uint64_t policy = policy_evict_normal();
@@ -412,33 +465,32 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         return __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
       };
       uint32_t t = 0;                                  // tile
+      AttnRing<C::kSlots> rg(is_k ? 0 : 2);
       bool ok = true;
       while (ok && w.next(a, units)) {
         int next_page = a.use_tma ? page_of(w, w.q.start + w.t0 * a.tile_keys) : -1;
-        for (int tile = w.t0; tile < w.t1; ++tile, ++t) {
+        for (int tile = w.t0; tile < w.t1; ++tile, rg.advance(is_k && t == 0 ? 1 : 2), ++t) {
           const int k0 = w.q.start + tile * a.tile_keys;
           const int page = next_page;
           if (a.use_tma && tile + 1 < w.t1) next_page = page_of(w, k0 + a.tile_keys);
-          const uint32_t i = 2 * t + (is_k ? 0 : 1);   // ring index
-          uint64_t *const bar = full + i % C::kSlots;
-          const uint32_t dst = ring + (i % C::kSlots) * C::kSlot;
-          ok = i < (uint32_t)C::kSlots ||
-               attn_wait(empty + i % C::kSlots, (i / C::kSlots + 1) & 1, abort_flag);
-          ok = __all_sync(FULL, ok);
+          uint64_t *const bar = full + rg.slot;
+          uint8_t *const to = s_ring + rg.slot * C::kSlot;
+          const uint32_t dst = smem_u32(to);
+          ok = __all_sync(FULL, attn_wait(empty + rg.slot, rg.phase ^ 1, abort_flag));
           if (!ok) break;
           if (a.use_tma && __all_sync(FULL, lane >= boxes || (page >= 0 && page < a.num_pages))) {
             if (is_k && lane < KT / 32)
               masks[(t % ATTN_MASKS) * 4 + lane] = bit_range(0, a.tile_keys, lane);
             __syncwarp();
             if (lane == 0) mbar_expect_tx(bar, (uint32_t)a.tile_keys * D * 2);
+            else mbar_arrive(bar);
             __syncwarp();
             // lane = page + boxes * column block (32 boxes at most)
             const int pg = lane % boxes, c = lane / boxes;
             const int id = __shfl_sync(FULL, page, pg);
             if (c < D / 64)
-              tma_load_2d(attn_smem + (dst - smem_u32(attn_smem)) + c * KT * 128 + pg * box_rows * 128,
-                          map, c * 64, (id * a.Hkv + w.kvh) * a.page_size + k0 % a.page_size, bar, policy);
-            mbar_arrive(bar);
+              tma_load_2d(to + c * KT * 128 + pg * box_rows * 128, map, c * 64,
+                          (id * a.Hkv + w.kvh) * a.page_size + k0 % a.page_size, bar, policy);
           } else {
             uint32_t idx[KT / 32];                     // rows lane + 32 c of the cache
 #pragma unroll
@@ -466,88 +518,96 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 cp_async16_zfill(dst + attn_place(u, r, KT), cache + (live ? (size_t)row * D : 0) + u * 8, live);
               }
             }
+            __syncwarp();                              // (the masks are written)
             cp_async_arrive_noinc(bar);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
           }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) issued[is_k ? 0 : 1] = t;
-    } else if (warp == 4) {
+    } else if (warp == MMA_WARP) {
       // ---------------------------------------------------------------- MMA --
-      if (lane == 0) {
-        const uint32_t ring = smem_u32(s_ring), q = smem_u32(s_q);
-        constexpr uint32_t kIdS = idesc_bf16(KT, 0), kIdO = idesc_bf16(D, 1);
-        uint32_t i = 0, t = 0, seg = 0;
-        bool ok = true;
-        auto ready = [&]() {
-          if (!attn_wait(full + i % C::kSlots, (i / C::kSlots) & 1, abort_flag)) return false;
-          fence_proxy_async();         // cp.async wrote through the generic proxy
+      const uint32_t ring = smem_u32(s_ring), q = smem_u32(s_q);
+      const uint32_t tm = __shfl_sync(FULL, tmem, 0);    // (uniform for the compiler too)
+      constexpr uint32_t kIdS = idesc_bf16(KT, 0), kIdO = idesc_bf16(D, 1);
+      uint32_t t = 0, seg = 0;
+      AttnRing<C::kSlots> kr(0), vr(2);
+      bool ok = true;                                    // (lanes agree after a vote per tile)
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = ok && attn_wait(bar, parity, abort_flag);
+      };
+      // S[tt & 1] = Q K^T, its K tile waited for
+      auto scores = [&](uint32_t tt) {
+        const uint64_t qd = smem_desc(q, 16, 1024, kSwizzle128B);
+        const uint64_t kd = smem_desc(ring + kr.slot * C::kSlot, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)                 // (descriptors count 16 bytes)
+          mma_f16_ss(tm + C::kS + (tt & 1) * KT, qd + ((c >> 2) * ATTN_ROWS * 128 + (c & 3) * 32) / 16,
+                     kd + ((c >> 2) * KT * 128 + (c & 3) * 32) / 16, kIdS, c > 0);
+        mma_commit(empty + kr.slot);
+        mma_commit(s_full + (tt & 1));
+        kr.advance(tt ? 2 : 1);
+      };
+      while (ok && w.next(a, units)) {
+        const uint32_t t_first = t, t_end = t + __shfl_sync(FULL, (uint32_t)(w.t1 - w.t0), 0);
+        wait(q_full, seg & 1);
+        // tile t is scored as soon as the softmax has read tile t - 2 from its
+        // place, two tiles ahead of its product with V
+        for (uint32_t tt = t; tt < t_end + 2; ++tt) {
+          if (tt < t_end) {
+            if (tt >= 2) wait(s_free + (tt & 1), ((tt - 2) >> 1) & 1);
+            wait(full + kr.slot, kr.phase);
+            ok = __all_sync(FULL, ok);
+            if (!ok) break;
+            fence_proxy_async();                         // (cp.async: the generic proxy)
+            tc_fence_after();
+            scores(tt);
+          }
+          if (tt < t_first + 2) continue;
+          wait(p_full + (t & 1), (t >> 1) & 1);
+          wait(full + vr.slot, vr.phase);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          fence_proxy_async();
           tc_fence_after();
-          return true;
-        };
-        // S[t] = Q K^T; K tiles sit at even ring indices 2t, V tiles at 2t + 1
-        auto scores = [&](uint32_t tt) {
-          i = 2 * tt;
-          if (!ready()) return false;
-          const uint32_t k = ring + (i % C::kSlots) * C::kSlot;
+          const uint64_t vd = smem_desc(ring + vr.slot * C::kSlot, KT * 128, 1024, kSwizzle128B);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint32_t ofs = (c & 3) * 32;
-            mma_f16_ss(tmem + C::kS + (tt & 1) * KT,
-                       smem_desc(q + (c >> 2) * ATTN_ROWS * 128 + ofs, 16, 1024, kSwizzle128B),
-                       smem_desc(k + (c >> 2) * KT * 128 + ofs, 16, 1024, kSwizzle128B), kIdS, c > 0);
-          }
-          tc_commit(empty + i % C::kSlots);
-          tc_commit(s_full + (tt & 1));
-          return true;
-        };
-        while (ok && w.next(a, units)) {
-          const uint32_t t_end = t + (uint32_t)(w.t1 - w.t0), t_first = t;
-          ok = attn_wait(q_full, seg & 1, abort_flag) && scores(t);
-          for (; ok && t < t_end; ++t) {
-            if (t + 1 < t_end) {
-              ok = scores(t + 1);
-            }
-            ok = ok && attn_wait(p_full + (t & 1), (t >> 1) & 1, abort_flag);
-            if (!ok) break;
-            i = 2 * t + 1;
-            ok = ready();
-            if (!ok) break;
-            const uint32_t v = ring + (i % C::kSlots) * C::kSlot;
-#pragma unroll
-            for (int c = 0; c < KT / 16; ++c)
-              mma_f16_ts(tmem + C::kO, tmem + C::kP + (t & 1) * (KT / 2) + c * 8,
-                         smem_desc(v + c * 2048, KT * 128, 1024, kSwizzle128B), kIdO,
-                         t > t_first || c > 0);
-            tc_commit(empty + i % C::kSlots);
-            tc_commit(pv_done + (t & 1));
-          }
-          ++seg;
+          for (int c = 0; c < KT / 16; ++c)
+            mma_f16_ts(tm + C::kO + (WGS == 2 ? (t & 1) * D : 0), tm + C::kP + (t & 1) * (KT / 2) + c * 8,
+                       vd + c * 2048 / 16, kIdO, t >= t_first + WGS || c > 0);
+          mma_commit(empty + vr.slot);
+          mma_commit(pv_done + (t & 1));
+          vr.advance(2);
+          ++t;
         }
-        tc_commit(drain);
-        mbar_wait_drain(drain, 0);
+        ++seg;
       }
-      __syncwarp();
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0);
     } else {
       // ------------------------------------------------------------ softmax --
-      constexpr int NC = C::NC;
-      const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-      const int kq = tid / C::RG;                           // lane group: keys [kq NC, +NC) of a tile
+      constexpr int NC = C::NC, GROUPS = WGS * KS;
+      constexpr int PART = WGS == 1 || NC < 64 ? NC : 64;   // scores held at a time
+      const int wg = warp >> 2, lid = tid & 127;            // warpgroup, tensor-memory lane
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const int kq = lid / C::RG, r = lid % C::RG;          // lane group: keys [kq NC, +NC) of a tile
       if (KS > 1) {                                         // weights of the other groups' keys: 0
         uint32_t zero[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) zero[e] = 0;
+        if (wg == 0) {
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) tc_st32(lanes + C::kP + c * 32, zero);
-        tc_wait_st();
+          for (int c = 0; c < KT / 32; ++c) tc_st32(lanes + C::kP + c * 32, zero);
+          tc_wait_st();
+        }
+        tc_fence_before();
+        softmax_sync<C::kSoftmax>();
+        tc_fence_after();
       }
       uint32_t t = 0;
-      const int r = tid % C::RG;
-      // A segment's queries, each warp the rows of its lanes (rows past the last
-      // are left as they are: they reach no output).  Called once all score MMAs
-      // of the segment before are complete.
+      // A segment's queries, each warp rows of its lanes (rows past the last are
+      // left as they are: they reach no output).  Called once all score MMAs of
+      // the segment before are complete.
       auto load_q = [&](const AttnWalk &g) {
         constexpr int UNITS = D / 8, RPP = 32 / UNITS;
         const int row = g.rb * ATTN_ROWS + r;
@@ -557,18 +617,34 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           const int at = row < a.rows ? (tok * a.Hq + g.kvh * group + row - tok * group) * D : -1;
           const uint32_t dst = smem_u32(s_q);
 #pragma unroll 8
-          for (int j = 0; j < 32 / RPP; ++j) {
-            const int from = __shfl_sync(FULL, at, j * RPP + r0);
+          for (int jj = 0; jj < 32 / RPP / WGS; ++jj) {
+            const int rr = (jj * WGS + wg) * RPP + r0;
+            const int from = __shfl_sync(FULL, at, rr);
             if (from >= 0)
-              cp_async16_zfill(dst + attn_place(u, warp * 32 + j * RPP + r0, ATTN_ROWS),
-                               src + from + u * 8, true);
+              cp_async16_zfill(dst + attn_place(u, (warp & 3) * 32 + rr, ATTN_ROWS), src + from + u * 8,
+                               true);
           }
         }
         cp_async_arrive_noinc(q_full);
       };
+      // columns [c, c + PART) of S, keys that the row does not see at -infinity
+      auto load_s = [&](uint32_t at, int c, const uint32_t *vis, bool all, uint32_t (&s)[PART]) {
+        if constexpr (PART == 16) {
+          tc_ld16_nowait(at, s);
+        } else {
+#pragma unroll
+          for (int h = 0; h < PART / 32; ++h) tc_ld32(at + c + h * 32, s + h * 32);
+        }
+        tc_wait_ld();
+        if (!all) {
+#pragma unroll
+          for (int e = 0; e < PART; ++e)
+            if (!((vis[(c + e) / 32] >> (e & 31)) & 1)) s[e] = 0xff800000u;
+        }
+      };
       bool more = w.next(a, units);
       if (more) load_q(w);
-      beside(&w);
+      beside(more ? &w : nullptr);
       while (more) {
         const int row = w.rb * ATTN_ROWS + r;
         const bool warp_live = row - lane < a.rows;
@@ -579,36 +655,36 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         bool ok = true;
         const uint32_t t_first = t, t_end = t + (uint32_t)(w.t1 - w.t0);
         for (; t < t_end; ++t) {
+          if (WGS == 2 && (int)(t & 1) != wg) continue;     // the other warpgroup's tile
           ok = attn_wait(s_full + (t & 1), (t >> 1) & 1, abort_flag);
           ok = __all_sync(FULL, ok);
           if (!ok) break;
           tc_fence_after();
           if (warp_live) {
-            uint32_t s[NC];
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-              tc_ld32(lanes + C::kS + (t & 1) * KT + kq * NC + c * 32, s + c * 32);
             const int k0 = w.q.start + (w.t0 + (int)(t - t_first)) * a.tile_keys + kq * NC;
-            uint32_t vis[NC / 32];
+            const uint32_t at = lanes + C::kS + (t & 1) * KT + kq * NC;
+            constexpr int WORDS = NC < 32 ? 1 : NC / 32;
+            constexpr uint32_t FULL_WORD = NC < 32 ? (1u << (NC & 31)) - 1u : 0xffffffffu;
+            uint32_t vis[WORDS];                            // this group's keys, a bit each
             bool all = k0 + NC - 1 <= w.q.n - a.N && (a.window == 0 || k0 > w.q.n - 1 - a.window);
 #pragma unroll
-            for (int c = 0; c < NC / 32; ++c) {
-              vis[c] = masks[(t % ATTN_MASKS) * 4 + kq * (NC / 32) + c];
-              all = all && vis[c] == 0xffffffffu;
+            for (int c = 0; c < WORDS; ++c) {
+              const int key = kq * NC + c * 32;
+              vis[c] = (masks[(t % ATTN_MASKS) * 4 + key / 32] >> (key & 31)) & FULL_WORD;
+              all = all && vis[c] == FULL_WORD;
             }
-            tc_wait_ld();
             if (!all) {
 #pragma unroll
-              for (int c = 0; c < NC / 32; ++c) {
-                vis[c] &= bit_range(see_lo - k0, pos + 1 - k0, c);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((vis[c] >> e) & 1)) s[c * 32 + e] = 0xff800000u;      // -infinity
-              }
+              for (int c = 0; c < WORDS; ++c) vis[c] &= bit_range(see_lo - k0, pos + 1 - k0, c);
             }
+            uint32_t s[PART];
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < NC; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+            for (int c = 0; c < NC; c += PART) {
+              load_s(at, c, vis, all, s);
+#pragma unroll
+              for (int e = 0; e < PART; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+            }
             const float top =
                 fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             // raise the maximum only where a weight would pass 2^8
@@ -616,34 +692,26 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             if (__any_sync(FULL, raise)) {
               const float mn = raise ? top : m;
               const float f = raise ? exp2_approx(m - mn) : 1.f;     // m = -inf: 0
-              if (t > t_first) {
-                ok = attn_wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+              if (t >= t_first + WGS) {
+                ok = attn_wait(pv_done + ((t - WGS) & 1), ((t - WGS) >> 1) & 1, abort_flag);
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t ot = lanes + C::kO + (uint32_t)wg * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                   uint32_t o[32];
-                  tc_ld32(lanes + C::kO + c * 32, o);
+                  tc_ld32(ot + c * 32, o);
                   tc_wait_ld();
 #pragma unroll
                   for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tc_st32(lanes + C::kO + c * 32, o);
+                  tc_st32(ot + c * 32, o);
                 }
               }
               l *= f;
               m = mn;
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < NC; e += 2) {
-              const float p0 = exp2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -base));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -base));
-              sum[(e >> 1) & 3] += p0 + p1;
-              s[e >> 1] = cvt_bf16x2(p0, p1);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (t >= 2) {                         // P[t & 1] is free once PV(t-2) is done
               ok = attn_wait(pv_done + (t & 1), ((t - 2) >> 1) & 1, abort_flag);
               ok = __all_sync(FULL, ok);
@@ -651,143 +719,135 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
               tc_fence_after();
             }
             const uint32_t pt = lanes + C::kP + (t & 1) * (KT / 2) + kq * (NC / 2);
-            if constexpr (NC == 32) {
-              tc_st16(pt, s);
-            } else {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < NC / 64; ++c) tc_st32(pt + c * 32, s + c * 32);
+            for (int c = 0; c < NC; c += PART) {
+              if (NC > PART) load_s(at, c, vis, all, s);
+              if (c + PART == NC) {                         // S is read: the next tile may come
+                tc_fence_before();
+                mbar_arrive(s_free + (t & 1));
+              }
+#pragma unroll
+              for (int e = 0; e < PART; e += 2) {
+                const float p0 = exp2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -base));
+                const float p1 = exp2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -base));
+                sum[(e >> 1) & 3] += p0 + p1;
+                s[e >> 1] = cvt_bf16x2(p0, p1);
+              }
+              if constexpr (PART == 16) tc_st_x8(pt, reinterpret_cast<const uint32_t(&)[8]>(s));
+              else if constexpr (PART == 32) tc_st16(pt, s);
+              else {
+#pragma unroll
+                for (int h = 0; h < PART / 64; ++h) tc_st32(pt + c / 2 + h * 32, s + h * 32);
+              }
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tc_wait_st();
+          } else {
+            mbar_arrive(s_free + (t & 1));
           }
           tc_fence_before();
           mbar_arrive(p_full + (t & 1));
         }
-        // ---- the segment's end: O / l to out, or O, m, l to the workspace; the
-        // next segment's queries on their way ----
+        // ---- the segment's end: once all its score MMAs are complete, the next
+        // segment's queries; then O / l to out, or O, m, l to the workspace ----
         AttnWalk ahead = w;
         more = ahead.next(a, units);
-        if (ok) {
-          if (more) load_q(ahead);
-          ok = attn_wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+        t = t_end;
+        if (ok && WGS == 2) ok = attn_wait(s_full + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+        ok = __all_sync(FULL, ok);
+        if (ok && more) load_q(ahead);
+        // this warpgroup's last tile: t - 1, or the one before; none in a segment
+        // of the other's single tile
+        const uint32_t mine = WGS == 1 || (int)((t - 1) & 1) == wg ? t - 1 : t - 2;
+        const bool had = mine + 1 > t_first;                // (mine may be t_first - 1 = ~0)
+        if (ok && had) {
+          ok = attn_wait(pv_done + (mine & 1), (mine >> 1) & 1, abort_flag);
           ok = __all_sync(FULL, ok);
         }
-        if (KS > 1) ok = softmax_all(ok);
+        ok = softmax_all<C::kSoftmax>(ok);
         if (!ok) break;
         tc_fence_after();
+        // The warpgroups' and lane groups' shares of a row meet in shared memory,
+        // 32 dims at a time; 8 threads then add up and write a row's quads.
         const bool whole = w.t0 == 0 && w.t1 == w.q.tiles, live = row < a.rows;
         const int slot = 2 * (int)blockIdx.x + (w.t0 == 0 ? 1 : 0);
-        uint16_t *const dst =
-            a.out + (((size_t)w.s * a.N + tok) * a.Hq + w.kvh * group + (row - tok * group)) * D;
-        float4 *const part = a.part_o + ((size_t)slot * a.rows_cap + r) * (D / 4);
-        if constexpr (KS == 1) {
+        float2 *const ml = reinterpret_cast<float2 *>(scratch);
+        ml[tid] = make_float2(m, l);
+        if (wg == 0 && kq == 0) row_at[r] = live ? (tok * a.Hq + row - tok * group) * D : -1;
+        softmax_sync<C::kSoftmax>();
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) top = fmaxf(top, ml[g * C::RG + r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const float2 x = ml[g * C::RG + r];
+          sum += exp2_approx(x.x - base) * x.y;
+        }
+        const float f = exp2_approx(m - base) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+        if (!whole && live && wg == 0 && kq == 0)
+          a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(top, sum);
+        softmax_sync<C::kSoftmax>();
+        uint16_t *const item = a.out + ((size_t)w.s * a.N * a.Hq + w.kvh * group) * D + (tid & 7) * 4;
+        float4 *const piece = a.part_o + (size_t)slot * a.rows_cap * (D / 4) + (tid & 7);
+        const int rows = min(C::RG, a.rows - w.rb * ATTN_ROWS);
+        const uint32_t ot = lanes + C::kO + (uint32_t)wg * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
           if (warp_live) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;      // l = 0: no key seen, O sums zeros
-            if (!whole && live) a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(m, l);
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc_ld32(lanes + C::kO + c * 32, o);
+            uint32_t o[32];
+            if (had) {
+              tc_ld32(ot + c * 32, o);
               tc_wait_ld();
-              if (!live) continue;
-              const float f = whole ? inv : 1.f;
-              auto quad = [&](int e) {
-                return make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                   __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
-              };
-#pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const float4 x = quad(e), y = quad(e + 1);
-                if (whole) {
-                  *reinterpret_cast<uint4 *>(dst + c * 32 + 4 * e) =
-                      make_uint4(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w), cvt_bf16x2(y.x, y.y),
-                                 cvt_bf16x2(y.z, y.w));
-                } else {
-                  part[c * 8 + e] = x;
-                  part[c * 8 + e + 1] = y;
-                }
-              }
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              scratch[e * C::kPitch + tid] =
+                  had ? make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                    __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
           }
-        } else {
-          // the lane groups' shares of a row meet in shared memory, 64 dims at a
-          // time; 16 threads then add up and write a row's quads
-          constexpr int PITCH = C::kScratchPitch;
-          float2 *const ml = reinterpret_cast<float2 *>(scratch);
-          ml[tid] = make_float2(m, l);
-          if (kq == 0) row_at[r] = live ? (tok * a.Hq + row - tok * group) * D : -1;
-          softmax_sync();
-          float top = -INFINITY, sum = 0.f;
+          softmax_sync<C::kSoftmax>();
+          for (int rr = tid >> 3; rr < rows; rr += C::kSoftmax / 8) {
+            const float4 *const from = scratch + (tid & 7) * C::kPitch + rr;
+            float4 x = from[0];
 #pragma unroll
-          for (int g = 0; g < KS; ++g) top = fmaxf(top, ml[g * C::RG + r].x);
-          const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-          for (int g = 0; g < KS; ++g) {
-            const float2 x = ml[g * C::RG + r];
-            sum += exp2_approx(x.x - base) * x.y;
-          }
-          const float f = exp2_approx(m - base) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
-          if (!whole && live && kq == 0) a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(top, sum);
-          softmax_sync();
-          uint16_t *const item =
-              a.out + ((size_t)w.s * a.N * a.Hq + w.kvh * group) * D + (tid & 15) * 4;
-          float4 *const piece = a.part_o + (size_t)slot * a.rows_cap * (D / 4) + (tid & 15);
-          const int rows = min(C::RG, a.rows);
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t o[32];
-              tc_ld32(lanes + C::kO + c * 64 + h * 32, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                scratch[(h * 8 + e) * PITCH + tid] =
-                    make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
-                                __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+            for (int g = 1; g < GROUPS; ++g) {
+              const float4 y = from[g * C::RG];
+              x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
             }
-            softmax_sync();
-            for (int rr = tid >> 4; rr < rows; rr += 8) {
-              const float4 *const from = scratch + (tid & 15) * PITCH + rr;
-              float4 x = from[0];
-#pragma unroll
-              for (int g = 1; g < KS; ++g) {
-                const float4 y = from[g * C::RG];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-              }
-              if (whole)
-                *reinterpret_cast<uint2 *>(item + row_at[rr] + c * 64) =
-                    make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
-              else
-                piece[(size_t)rr * (D / 4) + c * 16] = x;
-            }
-            softmax_sync();
+            if (whole)
+              *reinterpret_cast<uint2 *>(item + row_at[rr] + c * 32) =
+                  make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
+            else
+              piece[(size_t)rr * (D / 4) + c * 8] = x;
           }
+          softmax_sync<C::kSoftmax>();
         }
         tc_fence_before();
         w = ahead;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else if (warp < 4) {
+  } else if (warp < MMA_WARP) {
     beside(nullptr);
   }
   tc_fence_before();
   __syncthreads();
   // after a wait that ran out: the copies still in flight into this CTA's memory
   if (*abort_flag && tid < C::kSlots) {
-    for (int v = 0; v < 2; ++v) {                       // the slot's last K and last V tile
-      int last = -1;
-      for (int t = 0; t < (int)issued[v]; ++t)
-        if ((2 * t + v) % C::kSlots == tid) last = 2 * t + v;
-      // (a later tile of the other kind in the slot means that this one landed)
-      int other = -1;
-      for (int t = 0; t < (int)issued[1 - v]; ++t)
-        if ((2 * t + 1 - v) % C::kSlots == tid) other = 2 * t + 1 - v;
-      if (last > other) mbar_wait_drain(full + tid, (uint32_t)(last / C::kSlots) & 1);
+    int last = -1;                                      // the last tile put into slot tid
+    for (int t = 0; t < (int)issued[0]; ++t) {
+      const int i = t ? 2 * t - 1 : 0;
+      if (i % C::kSlots == tid) last = max(last, i);
     }
+    for (int t = 0; t < (int)issued[1]; ++t)
+      if ((2 * t + 2) % C::kSlots == tid) last = max(last, 2 * t + 2);
+    if (last >= 0) mbar_wait_drain(full + tid, (uint32_t)(last / C::kSlots) & 1);
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == MMA_WARP) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(C::kCols));
@@ -970,7 +1030,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
         !make_map(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v_cache, D, rows, D * 2, 64, box))
       return MOE_ERR_CUDA;
   }
-  cudaError_t e = launch_pdl(attn_kernel<D, KS>, grid, ATTN_THREADS, C::kSmem, s, k_map, v_map, a);
+  cudaError_t e = launch_pdl(attn_kernel<D, KS>, grid, C::kThreads, C::kSmem, s, k_map, v_map, a);
   if (e == cudaSuccess)
     e = launch_pdl(attn_join_kernel<D>, 2 * grid, JOIN_THREADS, 0, s, a, (int)grid);
   if (e != cudaSuccess) {
@@ -985,7 +1045,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
 template <int D>
 inline int attn_dispatch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   a.rows = a.N * (a.Hq / a.Hkv);
-  return a.rows <= 32   ? attn_launch<D, D == 256 ? 2 : 4>(a, ws, sms, s)
+  return a.rows <= 32   ? attn_launch<D, 4>(a, ws, sms, s)
          : a.rows <= 64 ? attn_launch<D, 2>(a, ws, sms, s)
                         : attn_launch<D, 1>(a, ws, sms, s);
 }
