@@ -37,6 +37,7 @@
 #pragma once
 #include "common.cuh"
 #include "ffn_tc.cuh"
+#include "kv_append.cuh"
 
 namespace moe {
 
@@ -181,11 +182,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 
 // Bounded wait, inline: the softmax threads hold a tile of scores in
@@ -732,7 +728,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                 const float p0 = exp2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -base));
                 const float p1 = exp2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -base));
                 sum[(e >> 1) & 3] += p0 + p1;
-                s[e >> 1] = cvt_bf16x2(p0, p1);
+                s[e >> 1] = pack_bf16(p0, p1);
               }
               if constexpr (PART == 16) tc_st_x8(pt, reinterpret_cast<const uint32_t(&)[8]>(s));
               else if constexpr (PART == 32) tc_st16(pt, s);
@@ -819,7 +815,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             }
             if (whole)
               *reinterpret_cast<uint2 *>(item + row_at[rr] + c * 32) =
-                  make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
+                  make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
             else
               piece[(size_t)rr * (D / 4) + c * 8] = x;
           }
@@ -958,7 +954,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs 
       const int row = sp.rb * ATTN_ROWS + r0 + rr, tok = row / group;
       uint16_t *dst = a.out +
                       (((size_t)sp.s * a.N + tok) * a.Hq + sp.kvh * group + (row - tok * group)) * D + d4 * 4;
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     }
     __syncthreads();
   }

@@ -502,7 +502,9 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
   const AppendArgs a{qkv, N, Hq, Hkv, norm ? 1 : 0, q_weight, k_weight, eps, cos_sin, max_pos, rot,
                      interleaved ? 1 : 0, kv_len, block_table, max_pages, num_pages, page_size,
                      k_cache, v_cache, q_out};
-  return launched(launch_append<1>(a, S * N, D, (cudaStream_t)stream));
+  const DeviceInfo *dev = device_info();
+  if (!dev) return MOE_ERR_CUDA;
+  return launched(launch_append(a, S * N, D, dev->sms, (cudaStream_t)stream));
 }
 
 // -------------------------------------------------------------- attention --
