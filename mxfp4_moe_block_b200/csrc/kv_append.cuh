@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // grid (S*N tokens, groups of HPT * 256/(D/8) heads).  Each lane group takes
 // HPT heads of its token, so that the cosines and sines are read once for all.
 template <int D, int HPT>
-__global__ void __launch_bounds__(APPEND_THREADS)
+__global__ void __launch_bounds__(APPEND_THREADS, 4)
 kv_append_kernel(const AppendArgs a) {
   pdl_wait();
   pdl_trigger();
