@@ -592,7 +592,7 @@ int block_sample(const float *logits, int S, int K, int V, const float *temperat
     if (min_p) part.min_p += r0 / K;
     const int st = launched(launch_pdl_cluster(
         sample_kernel, dim3((unsigned)c, (unsigned)n), SAMPLE_THREADS,
-        sample_smem_bytes(slice, top_k || top_p), (unsigned)c, (cudaStream_t)stream, part));
+        sample_smem_bytes(slice, top_k || top_p || min_p), (unsigned)c, (cudaStream_t)stream, part));
     if (st != MOE_OK) return st;
   }
   return MOE_OK;

@@ -41,8 +41,9 @@ constexpr int SAMPLE_THREADS = 512;
 constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
 constexpr int SAMPLE_MAX_V = 393216;
 constexpr int SAMPLE_BUCKETS = 1024;     // two per thread
-constexpr int SAMPLE_LIST = 1024;        // tokens the first CTA sorts, two per thread
-constexpr int SAMPLE_SMALL_K = 256;      // top-k found from the threads' own maxima
+constexpr int SAMPLE_LIST = 2048;        // tokens the first CTA looks through, four per thread
+constexpr int SAMPLE_QUEUE = 160;        // a warp's kept tokens that wait for their weights
+constexpr int SAMPLE_SMALL_K = 128;      // top-k that the first CTA settles alone
 constexpr int SAMPLE_MAX_CLUSTER = 8;
 constexpr unsigned long long SAMPLE_ONE = 1ull << 40;
 
@@ -128,7 +129,7 @@ struct SampleRow {
     double redd[SAMPLE_WARPS];
     u64 wsum[SAMPLE_WARPS];
     Found found;
-    int list_n;
+    int list_n;                // tokens in this CTA's list
     int pos;
   };
 };
@@ -318,10 +319,43 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const bool by_k = k > 0 && k < V, by_p = p < 1.0;
   const u64 low = mp > 0.f ? (u64)((double)fminf(mp, 1.f) * (double)SAMPLE_ONE) : 0;
 
+  // Every kept token of a warp's part of the slice, weighed by f(place in val) with
+  // full warps: few are kept as a rule, and they wait in the warp's queue (in the
+  // list's place) until there is one for every lane.  `zero`: the others become 0.
+  const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
+  float least = z.below;                         // x - top below which no token is kept
+  auto for_queued = [&](auto f, bool zero = false) {
+    uint32_t *const queue = reinterpret_cast<uint32_t *>(list) + warp * SAMPLE_QUEUE;
+    const float at = thr ? key_logit(thr) : -INFINITY;              // (thr 0: nothing cut)
+    const int last = thr ? cut : 0x7fffffff, j1 = min(units, (warp + 1) * wu);
+    int waiting = 0;
+    auto serve = [&](int n) {                                       // the queue's last n
+      waiting -= n;
+      if (lane < n) f(queue[waiting + lane]);
+      __syncwarp();
+    };
+    for (int j = warp * wu + lane; j - lane < j1; j += 32) {
+      const float none = __int_as_float(0x7fffffff);
+      const float4 q = j < j1 ? val4[j] : make_float4(none, none, none, none);
+      float e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool keep = z.positive(e[i]) && e[i] - z.ftop >= least &&
+                          (e[i] > at || (e[i] == at && v0 + 4 * j + i <= last));
+        const unsigned who = __ballot_sync(FULL, keep);
+        if (keep) queue[waiting + __popc(who & lanemask_lt())] = (uint32_t)(4 * j + i);
+        else e[i] = 0.f;
+        waiting += __popc(who);
+      }
+      if (zero && j < j1) val4[j] = make_float4(e[0], e[1], e[2], e[3]);
+      __syncwarp();
+      while (waiting >= 32) serve(32);
+    }
+    if (waiting) serve(waiting);
+  };
+
   if (by_k || by_p) {
     SampleRow::Found *const lead = cluster.map_shared_rank(&sh.found, 0);
-    u64 *const lead_list = cluster.map_shared_rank(list, 0);
-    int *const lead_n = cluster.map_shared_rank(&sh.list_n, 0);
 
     // every token of the slice that is still kept
     auto for_kept = [&](auto f) {
@@ -342,7 +376,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     };
     auto clear = [&]() {
       for (int i = tid; i < SAMPLE_BUCKETS; i += SAMPLE_THREADS) h_cnt[i] = h_lo[i] = h_hi[i] = 0;
-      if (tid == 0) sh.list_n = 0;
       __syncthreads();
     };
     // The first CTA adds the CTAs' histograms and finds the bucket in which the
@@ -353,7 +386,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       cluster.sync();
       if (rank == 0) {
         u64 n[2] = {0, 0}, m[2] = {0, 0};
-        for (int r = 0; r < C; ++r) {
+#pragma unroll
+        for (int r = 0; r < SAMPLE_MAX_CLUSTER; ++r) {
+          if (r >= C) break;
           const uint32_t *rc = cluster.map_shared_rank(h_cnt, r);
           const uint2 cnt = *reinterpret_cast<const uint2 *>(rc + 2 * tid);
           n[0] += cnt.x;
@@ -384,67 +419,109 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       cluster.sync();
       return *lead;
     };
-    // a token to the first CTA's list
+    // a token to this CTA's list; all CTAs' together are sorted by the first
     auto push = [&](float l, int v) {
-      const int at = atomicAdd(lead_n, 1);
-      if (at < SAMPLE_LIST) lead_list[at] = ((u64)logit_key(l) << 32) | (uint32_t)~(uint32_t)v;
+      const int at = atomicAdd(&sh.list_n, 1);
+      if (at < SAMPLE_LIST) list[at] = ((u64)logit_key(l) << 32) | (uint32_t)~(uint32_t)v;
     };
-    // first CTA: the list's first n words in descending order
-    auto sort_list = [&](int n) {
-      int m = 32;
-      while (m < n) m <<= 1;
-      for (int i = n + tid; i < m; i += SAMPLE_THREADS) list[i] = 0;
-      if (m <= 128) {                            // ranks by counting, four threads to a word
-        __syncthreads();
-        u64 x = 0;
-        int r = 0;
-        if (tid < 4 * m) {
-          x = list[tid >> 2];
-          for (int i = tid & 3; i < m; i += 4) {
-            const u64 y = list[i];
-            r += y > x || (y == x && i < (tid >> 2));
-          }
+    auto list_total = [&]() {
+      int n = 0;
+      for (int r = 0; r < C; ++r) n += *cluster.map_shared_rank(&sh.list_n, r);
+      return n;
+    };
+    // ---- the first CTA's part: the lists' words (key, ~index), four to a thread,
+    // in registers; all are different, so a prefix of the ranking is the words at or
+    // above one of them ----
+    constexpr int PER = SAMPLE_LIST / SAMPLE_THREADS;
+    auto take_lists = [&](int n, u64 (&v)[PER]) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        int i = tid + j * SAMPLE_THREADS, r = 0;
+        v[j] = 0;
+        if (i >= n) continue;
+        int c = sh.list_n;
+        while (i >= c) {
+          i -= c;
+          c = *cluster.map_shared_rank(&sh.list_n, ++r);
         }
-        r += __shfl_xor_sync(FULL, r, 1);
-        r += __shfl_xor_sync(FULL, r, 2);
-        __syncthreads();
-        if (tid < 4 * m && (tid & 3) == 0) list[r] = x;
-        __syncthreads();
-        return;
+        v[j] = cluster.map_shared_rank(list, r)[i];
       }
-      for (int size = 2; size <= m; size <<= 1)  // a bitonic network
-        for (int d = size >> 1; d > 0; d >>= 1) {
-          __syncthreads();
-          for (int i = tid; i < m / 2; i += SAMPLE_THREADS) {
-            const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-            const u64 x0 = list[lo], x1 = list[hi];
-            if ((x0 < x1) == ((lo & size) == 0)) {
-              list[lo] = x1;
-              list[hi] = x0;
+    };
+    auto word_logit = [&](u64 v) { return key_logit((uint32_t)(v >> 32)); };
+    // The word down to which the words (0: none) reach `want` in count or mass.  A
+    // histogram over the range of those in question, as often as more than a
+    // warp's worth is left.
+    auto pick = [&](const u64 (&v)[PER], const u64 (&m)[PER], bool by_mass, u64 want) -> u64 {
+      u64 floor = 1, ceiling = ~0ull, above = 0;             // words in question, sum of those before
+      for (;;) {
+        u64 hi = 0, lo = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (v[j] >= floor && v[j] <= ceiling) {
+            hi = v[j] > hi ? v[j] : hi;
+            lo = ~v[j] > lo ? ~v[j] : lo;
+          }
+        hi = block_max(hi);
+        lo = ~block_max(lo);
+        if (hi <= lo) return hi;
+        const int width = 64 - __clzll((long long)(hi - lo)), shift = width > 10 ? width - 10 : 0;
+        clear();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (v[j] >= lo && v[j] <= hi) {
+            const int b = (int)((hi - v[j]) >> shift);
+            atomicAdd(h_cnt + b, 1u);
+            if (by_mass) {
+              const uint32_t x = (uint32_t)m[j], old = atomicAdd(h_lo + b, x);
+              const uint32_t y = (uint32_t)(m[j] >> 32) + (old + x < old ? 1u : 0u);
+              if (y) atomicAdd(h_hi + b, y);
             }
           }
+        __syncthreads();
+        u64 n[2], total;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          n[i] = by_mass ? ((u64)h_hi[2 * tid + i] << 32) + h_lo[2 * tid + i] : h_cnt[2 * tid + i];
+        u64 run = above + block_scan(n[0] + n[1], sh.red, total);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (run < want && want <= run + n[i]) {
+            sh.found.bucket = 2 * tid + i;
+            sh.found.count = (int)h_cnt[2 * tid + i];
+            sh.found.above = run;
+          }
+          run += n[i];
         }
-      __syncthreads();
-    };
-    auto listed = [&](int i) { return key_logit((uint32_t)(list[i] >> 32)); };
-    // first CTA: of the sorted list's first n tokens, the index of the last that
-    // top-p keeps, once `need` is the mass wanted (0: top_p of all n)
-    auto last_by_mass = [&](int n, u64 need, u64 (&m)[2]) -> int {
-      u64 total;
+        if (tid == 0) sh.pos = 0;
+        __syncthreads();
+        above = sh.found.above;
+        ceiling = hi - ((u64)sh.found.bucket << shift);
+        floor = ceiling - lo >= (1ull << shift) ? ceiling - ((1ull << shift) - 1) : lo;
+        const int count = sh.found.count;
+        if (count > 32) continue;
+        // the last few: ranks by comparing in one warp
+        u64 *const few = reinterpret_cast<u64 *>(h_cnt);
+        __syncthreads();                         // (the histogram is read)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[i] = 2 * tid + i < n ? mass_at(listed(2 * tid + i)) : 0;
-      const u64 before = block_scan(m[0] + m[1], sh.red, total);
-      if (need == 0) need = p > 0.0 ? (u64)ceil(p * (double)total) : 1;
-      if (need < 1) need = 1;
-      if (tid == 0) sh.pos = n - 1;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const u64 pm = before + (i ? m[0] : 0);
-        if (pm < need && need <= pm + m[i]) sh.pos = 2 * tid + i;
+        for (int j = 0; j < PER; ++j)
+          if (v[j] >= floor && v[j] <= ceiling) {
+            const int at = atomicAdd(&sh.pos, 1);
+            few[2 * at] = v[j];
+            few[2 * at + 1] = by_mass ? m[j] : 1;
+          }
+        __syncthreads();
+        if (warp == 0) {
+          const u64 mine = lane < count ? few[2 * lane] : 0;
+          u64 before = above;
+          for (int i = 0; i < count; ++i)
+            if (few[2 * i] > mine) before += few[2 * i + 1];
+          if (lane < count && before < want && want <= before + few[2 * lane + 1]) sh.red[0] = mine;
+        }
+        __syncthreads();
+        const u64 found = sh.red[0];
+        __syncthreads();
+        return found;
       }
-      __syncthreads();
-      return sh.pos;
     };
 
     const float by_logit = (SAMPLE_BUCKETS - 1) / 32.f;       // 1024 buckets over 32 logits
@@ -452,80 +529,80 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       return (int)fminf((top - l) * scale, (float)(SAMPLE_BUCKETS - 1));
     };
 
-    // ---- top-k whose tokens fit the list: the first CTA settles the row ----
-    // For small k the histogram takes every thread's own maximum alone: the
-    // bucket of the k-th of those lies no higher than that of the k-th token.
-    bool counted = false;
+    // ---- a small top-k: the first CTA settles the row ----
+    // The histogram takes every thread's own maximum alone: the bucket of the k-th
+    // of those lies no higher than that of the k-th token, and few tokens more than
+    // k lie above it.
     SampleRow::Found f{};
-    if (by_k && k <= SAMPLE_LIST) {
-      bool fits = false;
-      if (k <= SAMPLE_SMALL_K && !inf_row) {
-        clear();
-        if (most > -INFINITY) atomicAdd(h_cnt + level0(most, by_logit), 1u);
-        f = find(false, (u64)k, 0, 0, 0);
-        fits = f.bucket >= 0;
-      }
-      if (!fits) {
-        clear();
-        for_kept([&](float l, int) { atomicAdd(h_cnt + level0(l, by_logit), 1u); });
-        f = find(false, (u64)k, 0, 0, 0);
-        counted = true;
-        fits = f.bucket >= 0 && f.upto <= SAMPLE_LIST;
-      }
-      if (fits) {
+    if (by_k && k <= SAMPLE_SMALL_K && !inf_row) {
+      clear();
+      if (tid == 0) sh.list_n = 0;
+      if (most > -INFINITY) atomicAdd(h_cnt + level0(most, by_logit), 1u);
+      f = find(false, (u64)k, 0, 0, 0);
+      if (f.bucket >= 0) {
         for_kept([&](float l, int v) {
           if (level0(l, by_logit) <= f.bucket) push(l, v);
         });
         cluster.sync();
-        const int n = *lead_n;
-        cluster.barrier_arrive();                // (the list's length is read)
+        const int n = list_total();
         if (n <= SAMPLE_LIST) {
           if (rank == 0) {
-            sort_list(n);
-            u64 m[2];
-            const int nk = min(n, k);
-            const int last = last_by_mass(nk, by_p ? 0 : ~0ull, m);
-            double w = 0.0;
-            u64 mine = 0, total;
+            u64 v[PER], m[PER], total;
+            take_lists(n, v);
+            cluster.barrier_arrive();            // (the others' lists are read)
+            const u64 kth = pick(v, m, false, (u64)min(n, k));
+            u64 mine = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = 2 * tid + i;
-              if (r > last || (r > 0 && m[i] < low)) m[i] = 0;
-              else if (z.positive(listed(r))) w += z.weight(listed(r));
-              mine += m[i];
+            for (int j = 0; j < PER; ++j) {
+              if (v[j] < kth) v[j] = 0;
+              m[j] = v[j] ? mass_at(word_logit(v[j])) : 0;
+              mine += m[j];
             }
+            u64 last = kth;
+            if (by_p) {
+              block_scan(mine, sh.red, total);
+              u64 bar = p > 0.0 ? (u64)ceil(p * (double)total) : 1;
+              last = pick(v, m, true, bar < 1 ? 1 : bar);
+            }
+            // The few kept: their masses, and their weights in steps of 2^-50 (whole
+            // numbers again: the lists' order changes from run to run)
+            u64 *const kept = reinterpret_cast<u64 *>(h_cnt);        // (~index, mass) of each
+            if (tid == 0) sh.pos = 0;
+            __syncthreads();
+            mine = 0;
+            u64 fine = 0, fines;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(FULL, w, o);
-            if (lane == 0) sh.redd[warp] = w;
-            block_scan(mine, sh.red, total);     // (its barriers order sh.redd)
-            w = 0.0;
-            for (int j = 0; j < SAMPLE_WARPS; ++j) w += sh.redd[j];
+            for (int j = 0; j < PER; ++j) {
+              if (v[j] == 0 || v[j] < last) continue;
+              const float l = word_logit(v[j]);
+              if (l < top && m[j] < low) continue;
+              const int at = atomicAdd(&sh.pos, 1);
+              kept[2 * at] = (uint32_t)v[j];
+              kept[2 * at + 1] = m[j];
+              mine += m[j];
+              if (z.positive(l)) fine += sample_mass(z.weight(l) * 1024.0);
+            }
+            block_scan(mine, sh.red, total);
+            block_scan(fine, sh.red, fines);
             if (tid == 0) {
-              const u64 e = list[last];
-              sh.found.thr = (uint32_t)(e >> 32);
-              sh.found.cut = (int)~(uint32_t)e;
-              sh.found.inv = (float)(1.0 / w);
+              sh.found.thr = (uint32_t)(last >> 32);
+              sh.found.cut = (int)~(uint32_t)last;
+              sh.found.inv = (float)(1024.0 / (double)fines);
             }
-            if (a.token) {                       // the draw, along the indices
-              u64 *const ms = reinterpret_cast<u64 *>(h_cnt);
-              ms[2 * tid] = m[0];
-              ms[2 * tid + 1] = m[1];
-              __syncthreads();
-              for (int r = tid; r <= last; r += SAMPLE_THREADS)    // ~index above, place below
-                list[r] = (list[r] << 32) | (uint32_t)r;
-              sort_list(last + 1);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                m[i] = 2 * tid + i <= last ? ms[(uint32_t)list[2 * tid + i]] : 0;
-              u64 run = block_scan(m[0] + m[1], sh.red, total);
+            if (a.token) {                       // the draw: four threads to a token
               const u64 want = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (run <= want && want < run + m[i])
-                  a.token[row] = (int)~(uint32_t)(list[2 * tid + i] >> 32);
-                run += m[i];
-              }
+              const int count = sh.pos, i = tid >> 2;
+              u64 upto = 0;
+              if (i < count)
+                for (int j = tid & 3; j < count; j += 4)
+                  if (kept[2 * j] >= kept[2 * i]) upto += kept[2 * j + 1];
+              upto += __shfl_xor_sync(FULL, upto, 1);
+              upto += __shfl_xor_sync(FULL, upto, 2);
+              if ((tid & 3) == 0 && i < count && upto > want && upto - kept[2 * i + 1] <= want)
+                a.token[row] = (int)~(uint32_t)kept[2 * i];
             }
+          } else {
+            cluster.barrier_arrive();
           }
           cluster.barrier_wait();
           if (!probs) return;
@@ -553,7 +630,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           cluster.barrier_wait();
           return;
         }
-        cluster.barrier_wait();
+        cluster.sync();                          // (the lists' lengths are read)
       }
     }
 
@@ -564,7 +641,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       uint32_t khi = 0xffffffffu, klo = 0;       // keys in question
       int bits = -1;                             // bucket width, or the first level's scale
       u64 above = 0, mass_above = 0, bar = 0;
-      bool have = !by_mass && counted;           // the first level is there already
       for (;;) {
         // the bucket of a logit, -1 if it is not in question any more
         auto bucket_of = [&](float l) -> int {
@@ -572,60 +648,55 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           const uint32_t key = logit_key(l);
           return key < klo || key > khi ? -1 : (int)((khi - key) >> bits);
         };
-        if (!have) {
-          clear();
-          if (by_mass) {
+        clear();
+        if (tid == 0) sh.list_n = 0;
+        if (by_mass) {                           // (tokens without weight are not in question)
+          auto add = [&](float l, u64 m) {
+            const int b = z.positive(l) ? bucket_of(l) : -1;
+            if (b < 0) return;
+            atomicAdd(h_cnt + b, 1u);
+            const uint32_t lo = (uint32_t)m, old = atomicAdd(h_lo + b, lo);
+            const uint32_t hi = (uint32_t)(m >> 32) + (old + lo < old ? 1u : 0u);
+            if (hi) atomicAdd(h_hi + b, hi);
+          };
+          if (thr)
+            for_queued([&](uint32_t i) { add(val[i], sample_mass(z.weight(val[i]))); });
+          else
             for (int j = tid; j < units; j += SAMPLE_THREADS) {
               const float4 q = val4[j];
               const float e[4] = {q.x, q.y, q.z, q.w};
               u64 m[4];
-              // the four weights side by side: a double's latency is that of
-              // many others
+              // the four weights side by side: a double's latency is that of many others
 #pragma unroll
               for (int i = 0; i < 4; ++i) m[i] = sample_mass(z.weight(e[i]));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (!(e[i] == e[i])) continue;
-                if (thr) {
-                  const uint32_t key = logit_key(e[i]);
-                  if (key < thr || (key == thr && v0 + 4 * j + i > cut)) continue;
-                }
-                const int b = bucket_of(e[i]);
-                if (b < 0) continue;
-                atomicAdd(h_cnt + b, 1u);
-                if (!z.positive(e[i])) continue;
-                const uint32_t lo = (uint32_t)m[i], old = atomicAdd(h_lo + b, lo);
-                const uint32_t hi = (uint32_t)(m[i] >> 32) + (old + lo < old ? 1u : 0u);
-                if (hi) atomicAdd(h_hi + b, hi);
-              }
+              for (int i = 0; i < 4; ++i)
+                add(e[i], m[i]);
             }
-          } else {
-            for_kept([&](float l, int) {
-              const int b = bucket_of(l);
-              if (b >= 0) atomicAdd(h_cnt + b, 1u);
-            });
-          }
-          f = find(by_mass, want, above, mass_above, bar);
+        } else {
+          for_kept([&](float l, int) {
+            const int b = bucket_of(l);
+            if (b >= 0) atomicAdd(h_cnt + b, 1u);
+          });
         }
-        have = false;
+        f = find(by_mass, want, above, mass_above, bar);
         if (f.bucket < 0) return;                // fewer tokens than wanted (the rest is NaN)
         bar = f.bar;
         if (f.count <= SAMPLE_LIST) {
           cluster.sync();                        // (found is read; it takes the answer)
           for_kept([&](float l, int v) {
-            if (bucket_of(l) == f.bucket) push(l, v);
+            if ((!by_mass || z.positive(l)) && bucket_of(l) == f.bucket) push(l, v);
           });
           cluster.sync();
           if (rank == 0) {
-            const int n = min(sh.list_n, SAMPLE_LIST);
-            sort_list(n);
-            u64 m[2];
-            const int last =
-                by_mass ? last_by_mass(n, bar - f.mass_above, m) : (int)(want - f.above) - 1;
+            u64 v[PER], m[PER];
+            take_lists(min(list_total(), SAMPLE_LIST), v);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) m[j] = by_mass && v[j] ? mass_at(word_logit(v[j])) : 0;
+            const u64 last = pick(v, m, by_mass, by_mass ? bar - f.mass_above : want - f.above);
             if (tid == 0) {
-              const u64 e = list[max(0, min(last, n - 1))];
-              sh.found.thr = (uint32_t)(e >> 32);
-              sh.found.cut = (int)~(uint32_t)e;
+              sh.found.thr = (uint32_t)(last >> 32);
+              sh.found.cut = (int)~(uint32_t)last;
             }
           }
           cluster.sync();
@@ -640,7 +711,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         if (bits < 0) {
           u64 hi = 0, lo = 0;
           for_kept([&](float l, int) {
-            if (bucket_of(l) != f.bucket) return;
+            if ((by_mass && !z.positive(l)) || bucket_of(l) != f.bucket) return;
             const uint32_t key = logit_key(l);
             hi = key > hi ? key : hi;
             lo = (uint32_t)~key > lo ? (uint32_t)~key : lo;
@@ -705,14 +776,13 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   }
 
   // ---- sums over what is kept; warp w takes the w-th part of the slice ----
-  const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
   u64 mass = 0;
   double wsum = 0.0;
   {
     const int j1 = min(units, (warp + 1) * wu);
-    // kept(l, v): whether the threshold keeps a token.  A thread's masses add up
-    // below 2^52, so the bits above are dropped once at the end.
-    auto sums = [&](auto with_probs, auto least, auto kept) {
+    // Nothing cut: every token.  A thread's masses add up below 2^52, so the bits
+    // above are dropped once at the end.
+    auto sums = [&](auto with_probs) {
       for (int j = warp * wu + lane; j < j1; j += 32) {
         const float4 q = val4[j];
         float e[4] = {q.x, q.y, q.z, q.w};
@@ -722,8 +792,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const u64 m = sample_mass_bits(w[i]);
-          bool keep = z.positive(e[i]) && kept(e[i], v0 + 4 * j + i);
-          if constexpr (decltype(least)::value) keep = keep && (m & SAMPLE_MASK) >= low;
+          const bool keep = z.positive(e[i]);
           if (keep) mass += m;
           if constexpr (decltype(with_probs)::value) {
             if (keep) wsum += w[i];
@@ -737,15 +806,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     const std::true_type yes;
     const std::false_type no;
     if (thr || low) {
-      const float at = thr ? key_logit(thr) : -INFINITY;            // (thr 0: nothing cut)
-      const int last = thr ? cut : 0x7fffffff;
-      auto kept = [&](float l, int v) { return l > at || (l == at && v <= last); };
-      if (probs) sums(yes, yes, kept);
-      else sums(no, yes, kept);
+      // min-p in advance, with room for what float loses; exact by the mass
+      least = low ? (float)((log2((double)low) - 40.0) / z.c) * 1.0001f - 1e-30f : z.below;
+      for_queued([&](uint32_t i) {
+        const double w = z.weight(val[i]);
+        const u64 m = sample_mass(w);
+        const bool keep = m >= low;
+        mass += keep ? m : 0;
+        wsum += keep ? w : 0.0;
+        if (probs) val[i] = keep ? (float)w : 0.f;
+      }, probs != nullptr);
     } else {
-      auto kept = [](float, int) { return true; };
-      if (probs) sums(yes, no, kept);
-      else sums(no, no, kept);
+      if (probs) sums(yes);
+      else sums(no);
     }
     mass &= SAMPLE_MASK;
   }
@@ -829,6 +902,8 @@ inline int sample_cluster(int rows, int V, int sms) {
 inline int sample_slice(int V, int c) { return ((V + c - 1) / c + 3) / 4 * 4; }
 inline size_t sample_smem_bytes(int slice, bool filters) {
   return (size_t)(slice + 4) * 4 + (filters ? SAMPLE_BUCKETS * 12 + SAMPLE_LIST * 8 : 0);
+  static_assert(SAMPLE_WARPS * SAMPLE_QUEUE <= 2 * SAMPLE_LIST && SAMPLE_SMALL_K * 16 <= SAMPLE_BUCKETS * 12,
+                "what takes the list's and the histogram's place");
 }
 
 }  // namespace moe
