@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     most = fmaxf(most, fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));    // (skips NaN)
   }
   cluster.barrier_wait();
-  float top = key_logit((uint32_t)cluster_max(logit_key(most)));
+  uint32_t top_key = (uint32_t)cluster_max(logit_key(most));
+  float top = key_logit(top_key);
   // +infinity takes all mass: such a row counts as 0 there and -infinity elsewhere
   const bool inf_row = top == INFINITY;
   auto infinite = [&](float l) { return inf_row ? (l == INFINITY ? 0.f : l == l ? -INFINITY : l) : l; };
@@ -313,9 +314,16 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const SampleScale z(top, 1.4426950408889634 / T);
   auto mass_at = [&](float l) -> u64 { return z.positive(l) ? sample_mass(z.weight(l)) : 0; };
 
-  // ---- the threshold: kept are keys above thr, and at thr the tokens <= cut ----
-  uint32_t thr = 0;
-  int cut = 0x7fffffff;
+  // ---- the threshold: kept are logits above `at`, and at it the tokens <= last ----
+  float at = -INFINITY;
+  int last = 0x7fffffff;
+  bool cutting = false;
+  auto kept = [&](float l, int v) { return l > at || (l == at && v <= last); };      // (NaN: no)
+  auto cut_to = [&](uint32_t key, int v) {
+    at = key_logit(key);
+    last = v;
+    cutting = true;
+  };
   const bool by_k = k > 0 && k < V, by_p = p < 1.0;
   const u64 low = mp > 0.f ? (u64)((double)fminf(mp, 1.f) * (double)SAMPLE_ONE) : 0;
 
@@ -323,11 +331,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // full warps: few are kept as a rule, and they wait in the warp's queue (in the
   // list's place) until there is one for every lane.  `zero`: the others become 0.
   const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
+  bool many = false;                             // top-p keeps a sixth of the row or more
   float least = z.below;                         // x - top below which no token is kept
   auto for_queued = [&](auto f, bool zero = false) {
     uint32_t *const queue = reinterpret_cast<uint32_t *>(list) + warp * SAMPLE_QUEUE;
-    const float at = thr ? key_logit(thr) : -INFINITY;              // (thr 0: nothing cut)
-    const int last = thr ? cut : 0x7fffffff, j1 = min(units, (warp + 1) * wu);
+    const int j1 = min(units, (warp + 1) * wu);
     int waiting = 0;
     auto serve = [&](int n) {                                       // the queue's last n
       waiting -= n;
@@ -338,15 +346,20 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       const float none = __int_as_float(0x7fffffff);
       const float4 q = j < j1 ? val4[j] : make_float4(none, none, none, none);
       float e[4] = {q.x, q.y, q.z, q.w};
+      bool keep[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool keep = z.positive(e[i]) && e[i] - z.ftop >= least &&
-                          (e[i] > at || (e[i] == at && v0 + 4 * j + i <= last));
-        const unsigned who = __ballot_sync(FULL, keep);
-        if (keep) queue[waiting + __popc(who & lanemask_lt())] = (uint32_t)(4 * j + i);
-        else e[i] = 0.f;
-        waiting += __popc(who);
+      for (int i = 0; i < 4; ++i)
+        keep[i] = z.positive(e[i]) && e[i] - z.ftop >= least && kept(e[i], v0 + 4 * j + i);
+      if (__any_sync(FULL, keep[0] || keep[1] || keep[2] || keep[3])) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned who = __ballot_sync(FULL, keep[i]);
+          if (keep[i]) queue[waiting + __popc(who & lanemask_lt())] = (uint32_t)(4 * j + i);
+          waiting += __popc(who);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = keep[i] ? e[i] : 0.f;
       if (zero && j < j1) val4[j] = make_float4(e[0], e[1], e[2], e[3]);
       __syncwarp();
       while (waiting >= 32) serve(32);
@@ -363,15 +376,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         const float4 q = val4[j];
         const float e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!(e[i] == e[i])) continue;
-          const int v = v0 + 4 * j + i;
-          if (thr) {
-            const uint32_t key = logit_key(e[i]);
-            if (key < thr || (key == thr && v > cut)) continue;
-          }
-          f(e[i], v);
-        }
+        for (int i = 0; i < 4; ++i)
+          if (kept(e[i], v0 + 4 * j + i)) f(e[i]);
       }
     };
     auto clear = [&]() {
@@ -419,10 +425,24 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       cluster.sync();
       return *lead;
     };
-    // a token to this CTA's list; all CTAs' together are sorted by the first
-    auto push = [&](float l, int v) {
-      const int at = atomicAdd(&sh.list_n, 1);
-      if (at < SAMPLE_LIST) list[at] = ((u64)logit_key(l) << 32) | (uint32_t)~(uint32_t)v;
+    // kept tokens that pass a test (few do) to this CTA's list; the first CTA looks
+    // through all CTAs' together
+    auto collect = [&](auto test) {
+      for (int j = tid; j < units; j += SAMPLE_THREADS) {
+        const float4 q = val4[j];
+        const float e[4] = {q.x, q.y, q.z, q.w};
+        bool take[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take[i] = test(e[i]) && kept(e[i], v0 + 4 * j + i);
+        if (!(take[0] || take[1] || take[2] || take[3])) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (take[i]) {
+            const int to = atomicAdd(&sh.list_n, 1);
+            if (to < SAMPLE_LIST)
+              list[to] = ((u64)logit_key(e[i]) << 32) | (uint32_t)~(uint32_t)(v0 + 4 * j + i);
+          }
+      }
     };
     auto list_total = [&]() {
       int n = 0;
@@ -530,108 +550,114 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     };
 
     // ---- a small top-k: the first CTA settles the row ----
-    // The histogram takes every thread's own maximum alone: the bucket of the k-th
-    // of those lies no higher than that of the k-th token, and few tokens more than
-    // k lie above it.
+    // Every CTA lists its tokens down to the k-th largest of its threads' own maxima:
+    // the k first-ranked of the row are among them, and few more than k of each CTA.
     SampleRow::Found f{};
     if (by_k && k <= SAMPLE_SMALL_K && !inf_row) {
       clear();
-      if (tid == 0) sh.list_n = 0;
-      if (most > -INFINITY) atomicAdd(h_cnt + level0(most, by_logit), 1u);
-      f = find(false, (u64)k, 0, 0, 0);
-      if (f.bucket >= 0) {
-        for_kept([&](float l, int v) {
-          if (level0(l, by_logit) <= f.bucket) push(l, v);
-        });
-        cluster.sync();
-        const int n = list_total();
-        if (n <= SAMPLE_LIST) {
-          if (rank == 0) {
-            u64 v[PER], m[PER], total;
-            take_lists(n, v);
-            cluster.barrier_arrive();            // (the others' lists are read)
-            const u64 kth = pick(v, m, false, (u64)min(n, k));
-            u64 mine = 0;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-              if (v[j] < kth) v[j] = 0;
-              m[j] = v[j] ? mass_at(word_logit(v[j])) : 0;
-              mine += m[j];
-            }
-            u64 last = kth;
-            if (by_p) {
-              block_scan(mine, sh.red, total);
-              u64 bar = p > 0.0 ? (u64)ceil(p * (double)total) : 1;
-              last = pick(v, m, true, bar < 1 ? 1 : bar);
-            }
-            // The few kept: their masses, and their weights in steps of 2^-50 (whole
-            // numbers again: the lists' order changes from run to run)
-            u64 *const kept = reinterpret_cast<u64 *>(h_cnt);        // (~index, mass) of each
-            if (tid == 0) sh.pos = 0;
-            __syncthreads();
-            mine = 0;
-            u64 fine = 0, fines;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-              if (v[j] == 0 || v[j] < last) continue;
-              const float l = word_logit(v[j]);
-              if (l < top && m[j] < low) continue;
-              const int at = atomicAdd(&sh.pos, 1);
-              kept[2 * at] = (uint32_t)v[j];
-              kept[2 * at + 1] = m[j];
-              mine += m[j];
-              if (z.positive(l)) fine += sample_mass(z.weight(l) * 1024.0);
-            }
-            block_scan(mine, sh.red, total);
-            block_scan(fine, sh.red, fines);
-            if (tid == 0) {
-              sh.found.thr = (uint32_t)(last >> 32);
-              sh.found.cut = (int)~(uint32_t)last;
-              sh.found.inv = (float)(1024.0 / (double)fines);
-            }
-            if (a.token) {                       // the draw: four threads to a token
-              const u64 want = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
-              const int count = sh.pos, i = tid >> 2;
-              u64 upto = 0;
-              if (i < count)
-                for (int j = tid & 3; j < count; j += 4)
-                  if (kept[2 * j] >= kept[2 * i]) upto += kept[2 * j + 1];
-              upto += __shfl_xor_sync(FULL, upto, 1);
-              upto += __shfl_xor_sync(FULL, upto, 2);
-              if ((tid & 3) == 0 && i < count && upto > want && upto - kept[2 * i + 1] <= want)
-                a.token[row] = (int)~(uint32_t)kept[2 * i];
-            }
-          } else {
-            cluster.barrier_arrive();
-          }
-          cluster.barrier_wait();
-          if (!probs) return;
-          cluster.sync();
-          thr = lead->thr;
-          cut = lead->cut;
-          const float inv = lead->inv, at = key_logit(thr);
-          cluster.barrier_arrive();              // (read before the first CTA leaves)
-          write_probs([&](int j) {
-            const float4 q = val4[j];
-            float e[4] = {q.x, q.y, q.z, q.w};
-            const bool any = e[0] >= at || e[1] >= at || e[2] >= at || e[3] >= at;
-            if (!any) return make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float pv = 0.f;
-              if ((e[i] > at || (e[i] == at && v0 + 4 * j + i <= cut)) && z.positive(e[i])) {
-                const double w = z.weight(e[i]);
-                if (sample_mass(w) >= low) pv = (float)w * inv;
-              }
-              e[i] = pv;
-            }
-            return make_float4(e[0], e[1], e[2], e[3]);
-          });
-          cluster.barrier_wait();
-          return;
-        }
-        cluster.sync();                          // (the lists' lengths are read)
+      if (tid == 0) {
+        sh.list_n = 0;
+        sh.pos = SAMPLE_BUCKETS - 1;             // (fewer maxima than k: every token)
       }
+      if (most > -INFINITY) atomicAdd(h_cnt + level0(most, by_logit), 1u);
+      __syncthreads();
+      {
+        const uint2 n = *reinterpret_cast<const uint2 *>(h_cnt + 2 * tid);
+        u64 total;
+        const u64 run = block_scan((u64)n.x + n.y, sh.red, total);
+        if (run < (u64)k && (u64)k <= run + n.x + n.y) sh.pos = 2 * tid + (run + n.x < (u64)k);
+        __syncthreads();
+      }
+      const float down = sh.pos == SAMPLE_BUCKETS - 1 ? NAN : (float)(sh.pos + 1);
+      collect([&](float l) { return !((top - l) * by_logit >= down); });
+      cluster.sync();
+      const int n = list_total();
+      if (n <= SAMPLE_LIST) {
+        if (rank == 0) {
+          u64 v[PER], m[PER];
+          take_lists(n, v);
+          cluster.barrier_arrive();              // (the others' lists are read)
+          const u64 kth = pick(v, m, false, (u64)min(n, k));
+          // the k words and their masses, four threads to a word from here on
+          ulonglong2 *const few = reinterpret_cast<ulonglong2 *>(h_cnt);
+          if (tid == 0) sh.pos = 0;
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (v[j] >= kth) few[atomicAdd(&sh.pos, 1)] = make_ulonglong2(v[j], mass_at(word_logit(v[j])));
+          __syncthreads();
+          const int count = sh.pos, i = tid >> 2;
+          const ulonglong2 mine = i < count ? few[i] : make_ulonglong2(0, 0);
+          // sum of the masses of the words that pass a test against this one's
+          auto sum_of = [&](auto test) {
+            u64 x = 0;
+            for (int j = tid & 3; j < count; j += 4)
+              if (test(few[j])) x += few[j].y;
+            x += __shfl_xor_sync(FULL, x, 1);
+            x += __shfl_xor_sync(FULL, x, 2);
+            return x;
+          };
+          u64 lowest = kth;
+          if (by_p) {
+            const u64 all = sum_of([](const ulonglong2 &) { return true; });
+            u64 bar = p > 0.0 ? (u64)ceil(p * (double)all) : 1;
+            if (bar < 1) bar = 1;
+            const u64 upto = sum_of([&](const ulonglong2 &w) { return w.x >= mine.x; });
+            __syncthreads();
+            if (i < count && upto >= bar && upto - mine.y < bar) sh.red[0] = mine.x;
+            __syncthreads();
+            lowest = sh.red[0];
+          }
+          auto stays = [&](const ulonglong2 &w) {
+            return w.x >= lowest && (w.y >= low || (uint32_t)(w.x >> 32) == top_key);
+          };
+          // The weights in steps of 2^-50: whole numbers, since the lists' order
+          // changes from run to run.
+          const bool mine_stays = i < count && (tid & 3) == 0 && stays(mine);
+          const float l = word_logit(mine.x);
+          u64 fine = mine_stays && z.positive(l) ? sample_mass(z.weight(l) * 1024.0) : 0, fines;
+          block_scan(fine, sh.red, fines);
+          if (tid == 0) {
+            sh.found.thr = (uint32_t)(lowest >> 32);
+            sh.found.cut = (int)~(uint32_t)lowest;
+            sh.found.inv = (float)(1024.0 / (double)fines);
+          }
+          if (a.token) {
+            const u64 total = sum_of(stays);
+            const u64 want = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
+            const u64 upto = sum_of(
+                [&](const ulonglong2 &w) { return (uint32_t)w.x >= (uint32_t)mine.x && stays(w); });
+            if (mine_stays && upto > want && upto - mine.y <= want) a.token[row] = (int)~(uint32_t)mine.x;
+          }
+        } else {
+          cluster.barrier_arrive();
+        }
+        cluster.barrier_wait();
+        if (!probs) return;
+        cluster.sync();
+        cut_to(lead->thr, lead->cut);
+        const float inv = lead->inv;
+        cluster.barrier_arrive();                // (read before the first CTA leaves)
+        write_probs([&](int j) {
+          const float4 q = val4[j];
+          float e[4] = {q.x, q.y, q.z, q.w};
+          if (!(e[0] >= at || e[1] >= at || e[2] >= at || e[3] >= at))
+            return make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float pv = 0.f;
+            if (kept(e[i], v0 + 4 * j + i) && z.positive(e[i])) {
+              const double w = z.weight(e[i]);
+              if (sample_mass(w) >= low) pv = (float)w * inv;
+            }
+            e[i] = pv;
+          }
+          return make_float4(e[0], e[1], e[2], e[3]);
+        });
+        cluster.barrier_wait();
+        return;
+      }
+      cluster.sync();                            // (the lists' lengths are read)
     }
 
     // ---- one filter: the least prefix of what is kept with `want` tokens, or
@@ -659,7 +685,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
             const uint32_t hi = (uint32_t)(m >> 32) + (old + lo < old ? 1u : 0u);
             if (hi) atomicAdd(h_hi + b, hi);
           };
-          if (thr)
+          if (cutting)
             for_queued([&](uint32_t i) { add(val[i], sample_mass(z.weight(val[i]))); });
           else
             for (int j = tid; j < units; j += SAMPLE_THREADS) {
@@ -670,11 +696,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 #pragma unroll
               for (int i = 0; i < 4; ++i) m[i] = sample_mass(z.weight(e[i]));
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                add(e[i], m[i]);
+              for (int i = 0; i < 4; ++i) add(e[i], m[i]);
             }
         } else {
-          for_kept([&](float l, int) {
+          for_kept([&](float l) {
             const int b = bucket_of(l);
             if (b >= 0) atomicAdd(h_cnt + b, 1u);
           });
@@ -682,11 +707,22 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         f = find(by_mass, want, above, mass_above, bar);
         if (f.bucket < 0) return;                // fewer tokens than wanted (the rest is NaN)
         bar = f.bar;
+        if (by_mass) many = f.upto * 6 > (u64)V;
         if (f.count <= SAMPLE_LIST) {
           cluster.sync();                        // (found is read; it takes the answer)
-          for_kept([&](float l, int v) {
-            if ((!by_mass || z.positive(l)) && bucket_of(l) == f.bucket) push(l, v);
-          });
+          // (tested without the conversions and the logit's key)
+          if (bits < 0) {
+            const float from = (float)f.bucket;
+            const float to = f.bucket == SAMPLE_BUCKETS - 1 ? NAN : (float)(f.bucket + 1);
+            collect([&](float l) {
+              const float d = (top - l) * scale;
+              return d >= from && !(d >= to) && (!by_mass || z.positive(l));
+            });
+          } else {
+            const uint32_t up = khi - ((uint32_t)f.bucket << bits), width = (1u << bits) - 1;
+            const float from = key_logit(up), to = key_logit(up - klo > width ? up - width : klo);
+            collect([&](float l) { return l <= from && l >= to && (!by_mass || z.positive(l)); });
+          }
           cluster.sync();
           if (rank == 0) {
             u64 v[PER], m[PER];
@@ -700,8 +736,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
             }
           }
           cluster.sync();
-          thr = lead->thr;
-          cut = lead->cut;
+          cut_to(lead->thr, lead->cut);
           cluster.sync();                        // (found is free for the next filter)
           return;
         }
@@ -710,7 +745,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         mass_above = f.mass_above;
         if (bits < 0) {
           u64 hi = 0, lo = 0;
-          for_kept([&](float l, int) {
+          for_kept([&](float l) {
             if ((by_mass && !z.positive(l)) || bucket_of(l) != f.bucket) return;
             const uint32_t key = logit_key(l);
             hi = key > hi ? key : hi;
@@ -727,17 +762,17 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           const u64 one = by_mass ? mass_at(key_logit(khi)) : 1;
           const u64 take = by_mass ? (bar - mass_above + one - 1) / one : want - above;
           u64 mine = 0;
-          for_kept([&](float l, int) { mine += logit_key(l) == khi; });
+          for_kept([&](float l) { mine += logit_key(l) == khi; });
           u64 cnt;
           block_scan(mine, sh.red, cnt);
           const u64 *pc = exchange(cnt);
           u64 before = 0;
           for (int j = 0; j < rank; ++j) before += pc[j];
           // the CTA that holds the take-th of them finds its index
-          u64 at = 0;
+          u64 spot = 0;
           if (before < take && take <= before + cnt) {
             u64 run = before;
-            for (int b = 0; b < units && at == 0; b += SAMPLE_THREADS) {
+            for (int b = 0; b < units && spot == 0; b += SAMPLE_THREADS) {
               const int j = b + tid;
               const float4 q = j < units ? val4[j] : make_float4(NAN, NAN, NAN, NAN);
               const float e[4] = {q.x, q.y, q.z, q.w};
@@ -746,7 +781,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int v = v0 + 4 * j + i;
-                eq[i] = e[i] == e[i] && logit_key(e[i]) == khi && (khi > thr || v <= cut);
+                eq[i] = kept(e[i], v) && logit_key(e[i]) == khi;
                 n += eq[i];
               }
               u64 r = run + block_scan(n, sh.red, sum);
@@ -756,15 +791,14 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
               for (int i = 0; i < 4; ++i)
                 if (eq[i] && ++r == take) sh.pos = v0 + 4 * j + i;
               __syncthreads();
-              if (sh.pos >= 0) at = (u64)sh.pos + 1;
+              if (sh.pos >= 0) spot = (u64)sh.pos + 1;
               run += sum;
             }
           }
-          const u64 *pa = exchange(at);
+          const u64 *pa = exchange(spot);
           u64 sum = 0;
           for (int j = 0; j < C; ++j) sum += pa[j];
-          thr = khi;
-          cut = (int)sum - 1;
+          cut_to(khi, (int)sum - 1);
           return;
         }
         const int width = 32 - __clz(khi - klo);   // bits of the distance
@@ -780,9 +814,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   double wsum = 0.0;
   {
     const int j1 = min(units, (warp + 1) * wu);
-    // Nothing cut: every token.  A thread's masses add up below 2^52, so the bits
-    // above are dropped once at the end.
-    auto sums = [&](auto with_probs) {
+    // Every token, or most: each is weighed where it stands.  A thread's masses add
+    // up below 2^52, so the bits above are dropped once at the end.
+    auto sums = [&](auto with_probs, auto with_cut) {
       for (int j = warp * wu + lane; j < j1; j += 32) {
         const float4 q = val4[j];
         float e[4] = {q.x, q.y, q.z, q.w};
@@ -792,7 +826,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const u64 m = sample_mass_bits(w[i]);
-          const bool keep = z.positive(e[i]);
+          bool keep = z.positive(e[i]);
+          if constexpr (decltype(with_cut)::value)
+            keep = keep && kept(e[i], v0 + 4 * j + i) && (m & SAMPLE_MASK) >= low;
           if (keep) mass += m;
           if constexpr (decltype(with_probs)::value) {
             if (keep) wsum += w[i];
@@ -805,7 +841,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     };
     const std::true_type yes;
     const std::false_type no;
-    if (thr || low) {
+    if ((cutting || low) && !many) {
       // min-p in advance, with room for what float loses; exact by the mass
       least = low ? (float)((log2((double)low) - 40.0) / z.c) * 1.0001f - 1e-30f : z.below;
       for_queued([&](uint32_t i) {
@@ -816,9 +852,12 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         wsum += keep ? w : 0.0;
         if (probs) val[i] = keep ? (float)w : 0.f;
       }, probs != nullptr);
+    } else if (many) {
+      if (probs) sums(yes, yes);
+      else sums(no, yes);
     } else {
-      if (probs) sums(yes);
-      else sums(no);
+      if (probs) sums(yes, no);
+      else sums(no, no);
     }
     mass &= SAMPLE_MASK;
   }
@@ -872,8 +911,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   auto mass_of = [&](int v) -> u64 {
     // (weights took the logits' place in shared memory where probabilities are wanted)
     const float l = probs ? infinite(x[v]) : val[v - v0];
-    const uint32_t key = logit_key(l);
-    if (key < thr || (key == thr && v > cut)) return 0;
+    if (!kept(l, v)) return 0;
     const u64 mv = mass_at(l);
     return mv >= low ? mv : 0;
   };
