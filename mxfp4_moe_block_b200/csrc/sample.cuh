@@ -886,8 +886,31 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     total += pm[j];
     sum += sh.xchd[j];
   }
-  // no CTA leaves before every other has finished writing to it: the exchange
-  // above was the last remote access
+  // (no CTA leaves before every other has finished writing to it: the exchange
+  // above was the last remote access)
+
+  // ---- the draw: the CTA, the warp's part, then a few tokens to a thread, whose
+  // logits are on their way while the probabilities are written ----
+  const u64 m = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
+  const bool here = a.token != nullptr && before <= m && m < before + cta_mass;
+  int t0 = 0, t1 = 0;
+  constexpr int AHEAD = 4;
+  float ahead[AHEAD];
+  if (here) {
+    int part = 0;
+    for (u64 w = sh.wsum[0]; before + w <= m; w = sh.wsum[part]) {
+      before += w;
+      ++part;
+    }
+    const int b0 = max(c0, v0 + 4 * part * wu), b1 = min(c1, v0 + 4 * min(units, (part + 1) * wu));
+    const int each = (b1 - b0 + SAMPLE_THREADS - 1) / SAMPLE_THREADS;
+    t0 = min(b1, b0 + tid * each);
+    t1 = min(b1, t0 + each);
+    // (weights took the logits' place in shared memory where probabilities are wanted)
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      ahead[i] = t0 + i < t1 ? (probs ? x[t0 + i] : val[t0 + i - v0]) : 0.f;
+  }
   if (probs) {
     const float inv = (float)(1.0 / sum);
     write_probs([&](int j) {
@@ -895,37 +918,32 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       return make_float4(q.x * inv, q.y * inv, q.z * inv, q.w * inv);
     });
   }
-  if (!a.token) return;
-
-  // ---- the draw: the CTA, the warp's part, then a few tokens to a thread ----
-  const u64 m = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
-  if (!(before <= m && m < before + cta_mass)) return;
-  int part = 0;
-  for (u64 w = sh.wsum[0]; before + w <= m; w = sh.wsum[part]) {
-    before += w;
-    ++part;
-  }
-  const int b0 = max(c0, v0 + 4 * part * wu), b1 = min(c1, v0 + 4 * min(units, (part + 1) * wu));
-  const int each = (b1 - b0 + SAMPLE_THREADS - 1) / SAMPLE_THREADS;
-  const int t0 = min(b1, b0 + tid * each), t1 = min(b1, t0 + each);
-  auto mass_of = [&](int v) -> u64 {
-    // (weights took the logits' place in shared memory where probabilities are wanted)
-    const float l = probs ? infinite(x[v]) : val[v - v0];
+  if (!here) return;
+  auto mass_of = [&](int v, float l) -> u64 {
+    if (probs) l = infinite(l);
     if (!kept(l, v)) return 0;
     const u64 mv = mass_at(l);
     return mv >= low ? mv : 0;
   };
+  auto each_mass = [&](auto f) {                 // f(token, mass) -> whether to go on
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (t0 + i < t1 && !f(t0 + i, mass_of(t0 + i, ahead[i]))) return;
+    for (int v = t0 + AHEAD; v < t1; ++v)
+      if (!f(v, mass_of(v, probs ? x[v] : val[v - v0]))) return;
+  };
   u64 mine = 0, all;
-  for (int v = t0; v < t1; ++v) mine += mass_of(v);
+  each_mass([&](int, u64 mv) {
+    mine += mv;
+    return true;
+  });
   u64 run = before + block_scan(mine, sh.red, all);
   if (run <= m && m < run + mine)
-    for (int v = t0; v < t1; ++v) {
-      run += mass_of(v);
-      if (run > m) {
-        a.token[row] = v;
-        break;
-      }
-    }
+    each_mass([&](int v, u64 mv) {
+      run += mv;
+      if (run > m) a.token[row] = v;
+      return run <= m;
+    });
 }
 
 // CTAs of a row: slices of at most 18432 tokens (72 KB, two CTAs per SM) and,
