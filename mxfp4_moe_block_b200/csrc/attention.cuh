@@ -340,7 +340,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, 32);
+      mbar_init(full + i, 33);
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -441,10 +441,12 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
 
     if (warp >= K_WARP) {
       // ----------------------------------------------------- producers: K and V --
-      // A full tile of whole pages is a TMA box per page and 64 dims; a tile with
-      // keys outside [lo, n) or on a bad page, and pages that are no whole
-      // number of eight rows, go row by row through cp.async, which zero-fills
-      // what is outside.  Either way a slot's barrier gets an arrival a lane.
+      // A page is a TMA box per 64 dims.  Rows outside [lo, n) may hold anything:
+      // of K they come along (their scores are masked), of V, where a weight of 0
+      // times NaN would spoil the sum, pages with such rows go row by row through
+      // cp.async, which zero-fills them.  Pages that are no whole number of eight
+      // rows (the swizzle's period) all go that way.  A slot's barrier gets an arrival
+      // a lane, after its cp.asyncs, and one with the bytes that TMA brings.
       constexpr int UNITS = D / 8;                     // 16-byte units of a row
       constexpr int RPP = 32 / UNITS;                  // rows of one pass of the warp
       const bool is_k = warp == K_WARP;
@@ -454,46 +456,92 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       const uint64_t policy = policy_evict_normal();
       const int boxes = a.use_tma ? max(1, a.tile_keys / a.page_size) : 0;   // pages of a tile
       const int box_rows = a.use_tma ? a.tile_keys / boxes : 0;
-      // this lane's page of the tile whose first key is k0 (whole tiles only)
-      auto page_of = [&](const AttnWalk &w, int k0) -> int {
-        const int lp = k0 / a.page_size + lane;
-        if (lane >= boxes || k0 < w.q.lo || k0 + a.tile_keys > w.q.n) return -1;
-        return __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
+      // this lane's page of the tile whose first key is k0, -1 where no key is seen
+      auto page_of = [&](const AttnWalk &g, int k0) -> int {
+        const int first = k0 + lane * box_rows;
+        if (lane >= boxes || first + box_rows <= g.q.lo || first >= g.q.n) return -1;
+        return __ldg(a.block_table + (size_t)g.s * a.max_pages + first / a.page_size);
       };
+      auto first_key = [&](const AttnWalk &g) { return g.q.start + g.t0 * a.tile_keys; };
       uint32_t t = 0;                                  // tile
       AttnRing<C::kSlots> rg(is_k ? 0 : 2);
-      bool ok = true;
-      while (ok && w.next(a, units)) {
-        int next_page = a.use_tma ? page_of(w, w.q.start + w.t0 * a.tile_keys) : -1;
+      bool ok = true, more = w.next(a, units);
+      int next_page = more && a.use_tma ? page_of(w, first_key(w)) : -1;
+      while (ok && more) {
+        AttnWalk ahead = w;
+        more = ahead.next(a, units);
         for (int tile = w.t0; tile < w.t1; ++tile, rg.advance(is_k && t == 0 ? 1 : 2), ++t) {
           const int k0 = w.q.start + tile * a.tile_keys;
           const int page = next_page;
-          if (a.use_tma && tile + 1 < w.t1) next_page = page_of(w, k0 + a.tile_keys);
+          if (a.use_tma) {
+            if (tile + 1 < w.t1) next_page = page_of(w, k0 + a.tile_keys);
+            else if (more) next_page = page_of(ahead, first_key(ahead));
+          }
           uint64_t *const bar = full + rg.slot;
           uint8_t *const to = s_ring + rg.slot * C::kSlot;
           const uint32_t dst = smem_u32(to);
           ok = __all_sync(FULL, attn_wait(empty + rg.slot, rg.phase ^ 1, abort_flag));
           if (!ok) break;
-          if (a.use_tma && __all_sync(FULL, lane >= boxes || (page >= 0 && page < a.num_pages))) {
+          // lane = page + boxes * column block of 64 dims (32 boxes at most)
+          const int pg = lane % max(boxes, 1), c64 = lane / max(boxes, 1);
+          auto box = [&](int id) {
+            tma_load_2d(to + c64 * KT * 128 + pg * box_rows * 128, map, c64 * 64,
+                        (id * a.Hkv + w.kvh) * a.page_size + k0 % a.page_size, bar, policy);
+          };
+          if (a.use_tma && k0 >= w.q.lo && k0 + a.tile_keys <= w.q.n &&
+              __all_sync(FULL, lane >= boxes || (page >= 0 && page < a.num_pages))) {
             if (is_k && lane < KT / 32)
               masks[(t % ATTN_MASKS) * 4 + lane] = bit_range(0, a.tile_keys, lane);
             __syncwarp();
             if (lane == 0) mbar_expect_tx(bar, (uint32_t)a.tile_keys * D * 2);
-            else mbar_arrive(bar);
-            __syncwarp();
-            // lane = page + boxes * column block (32 boxes at most)
-            const int pg = lane % boxes, c = lane / boxes;
             const int id = __shfl_sync(FULL, page, pg);
-            if (c < D / 64)
-              tma_load_2d(to + c * KT * 128 + pg * box_rows * 128, map, c * 64,
-                          (id * a.Hkv + w.kvh) * a.page_size + k0 % a.page_size, bar, policy);
+            if (c64 < D / 64) box(id);
+            mbar_arrive(bar);
+          } else if (a.use_tma) {
+            // this lane's page: seen in part or whole, in the pool; brought by TMA
+            const int first = k0 + lane * box_rows;
+            const bool seen = lane < boxes && first + box_rows > w.q.lo && first < w.q.n;
+            const bool good = seen && page >= 0 && page < a.num_pages;
+            const bool whole = good && first >= w.q.lo && first + box_rows <= w.q.n;
+            if (seen && !good) raise_status(MOE_DEV_BAD_INDEX);
+            const unsigned tma = __ballot_sync(FULL, is_k ? good : whole);
+            const unsigned goods = __ballot_sync(FULL, good), bad = __ballot_sync(FULL, seen && !good);
+            if (is_k && lane < KT / 32) {              // masks: keys in [lo, n) on good pages
+              uint32_t m = bit_range(w.q.lo - k0, min(w.q.n - k0, a.tile_keys), lane);
+              for (unsigned b = bad; b; b &= b - 1) {
+                const int row0 = (__ffs(b) - 1) * box_rows;
+                m &= ~bit_range(row0, row0 + box_rows, lane);
+              }
+              masks[(t % ATTN_MASKS) * 4 + lane] = m;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(bar, (uint32_t)__popc(tma) * box_rows * D * 2);
+            __syncwarp();
+            const int id = __shfl_sync(FULL, page, pg);
+            if (c64 < D / 64 && ((tma >> pg) & 1)) box(id);
+            if (!is_k)                                 // the other pages' rows, or zeros
+              for (int pgv = 0; pgv < boxes; ++pgv) {
+                if ((tma >> pgv) & 1) continue;
+                const bool in = (goods >> pgv) & 1;
+                const int idv = __shfl_sync(FULL, page, pgv), row0 = pgv * box_rows;
+                const size_t base =
+                    in ? ((size_t)idv * a.Hkv + w.kvh) * a.page_size + (k0 + row0) % a.page_size : 0;
+#pragma unroll 4
+                for (int r = r0; r < box_rows; r += RPP) {
+                  const int key = k0 + row0 + r;
+                  const bool live = in && key >= w.q.lo && key < w.q.n;
+                  cp_async16_zfill(dst + attn_place(u, row0 + r, KT),
+                                   cache + (live ? (base + r) * D : 0) + u * 8, live);
+                }
+              }
+            cp_async_arrive_noinc(bar);
           } else {
             uint32_t idx[KT / 32];                     // rows lane + 32 c of the cache
 #pragma unroll
             for (int c = 0; c < KT / 32; ++c) {
               const int e = c * 32 + lane, key = k0 + e;
               idx[c] = 0xffffffffu;
-              if (e < a.tile_keys && key >= w.q.lo && key < w.q.n) {
+              if (key >= w.q.lo && key < w.q.n) {
                 const int lp = key / a.page_size;
                 const int id = __ldg(a.block_table + (size_t)w.s * a.max_pages + lp);
                 if (id >= 0 && id < a.num_pages)
@@ -515,9 +563,11 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
               }
             }
             __syncwarp();                              // (the masks are written)
+            if (lane == 0) mbar_arrive(bar);
             cp_async_arrive_noinc(bar);
           }
         }
+        w = ahead;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (lane == 0) issued[is_k ? 0 : 1] = t;
