@@ -913,7 +913,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs 
   pdl_trigger();
   constexpr int QUADS = D / 4;
   constexpr int MOST_ROWS = JOIN_THREADS / QUADS;        // G = 1
-  __shared__ float wgt[16 * ATTN_MAX_CTAS];
+  // rows x pieces of a unit: 4 MOST_ROWS x 4, MOST_ROWS / 2 x 16 or / 8 x 148 at most
+  __shared__ float wgt[MOST_ROWS / 8 * ATTN_MAX_CTAS];
+  static_assert(16 <= ATTN_MAX_CTAS / 8, "weights of few pieces");
   __shared__ float4 acc[JOIN_THREADS];
   __shared__ AttnSplit items[ATTN_MAX_CTAS];
   __shared__ int first[ATTN_MAX_CTAS + 1];               // units before an item
@@ -922,12 +924,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs 
   const int group = a.Hq / a.Hkv;
   // groups of pieces: a unit's weights (rows x pieces) fit `wgt` either way
   auto shift_of = [](int count) { return count > 16 ? 3 : count > 4 ? 1 : 0; };
+  auto rows_per_unit = [&](int count) { return count > 4 ? MOST_ROWS >> shift_of(count) : 4 * MOST_ROWS; };
   auto rows_of = [&](const AttnSplit &sp) { return min(ATTN_ROWS, a.rows - sp.rb * ATTN_ROWS); };
   int mine = 0;
   if (tid < pieces) {
     const AttnSplit sp = a.split[tid];
     items[tid] = sp;
-    const int rpu = MOST_ROWS >> shift_of(sp.count);
+    const int rpu = rows_per_unit(sp.count);
     mine = sp.count ? (rows_of(sp) + rpu - 1) / rpu : 0;
   }
   int upto = mine;
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs 
       else hi = mid;
     }
     const AttnSplit sp = items[lo];
-    const int sh = shift_of(sp.count), G = 1 << sh, rpu = MOST_ROWS >> sh;
+    const int G = 1 << shift_of(sp.count), rpu = rows_per_unit(sp.count);
     const int r0 = (u - first[lo]) * rpu, rows = min(rpu, rows_of(sp) - r0);
     auto slot = [&](int i) { return 2 * (size_t)(sp.first + i) + (i == 0 ? 1 : 0); };
     // the pieces' weights 2^(m_i - m) / l: a warp per row
@@ -979,32 +982,54 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnArgs 
       for (int j = 0; j < MOST; ++j)
         if (lane + 32 * j < sp.count) wgt[rr * sp.count + lane + 32 * j] = x[j].x * inv;
     }
-    const int d4 = tid % QUADS, rr = (tid / QUADS) % rpu, grp = tid / (rpu * QUADS);
     __syncthreads();
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (rr < rows) {
-      const float4 *x0 = a.part_o + (size_t)(r0 + rr) * QUADS + d4;
-#pragma unroll 4
-      for (int i = grp; i < sp.count; i += G) {
-        const float4 x = x0[slot(i) * QUADS * a.rows_cap];
-        const float f = wgt[rr * sp.count + i];
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
-      }
-    }
-    acc[tid] = o;
-    __syncthreads();
-    if (grp == 0 && rr < rows) {
-      for (int g = 1; g < G; ++g) {
-        const float4 x = acc[tid + g * rpu * QUADS];
-        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-      }
+    const int d4 = tid % QUADS;
+    auto add = [](float4 &o, const float4 &x, float f) {
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    };
+    auto store = [&](int rr, const float4 &o) {
       const int row = sp.rb * ATTN_ROWS + r0 + rr, tok = row / group;
       uint16_t *dst = a.out +
                       (((size_t)sp.s * a.N + tok) * a.Hq + sp.kvh * group + (row - tok * group)) * D + d4 * 4;
       *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    };
+    const size_t step = (size_t)QUADS * a.rows_cap;
+    if (sp.count <= 4) {                                 // four rows to a thread
+      float4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= sp.count) break;
+        const float4 *x = a.part_o + slot(i) * step + (size_t)r0 * QUADS + d4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = tid / QUADS + k * MOST_ROWS;
+          if (rr < rows) add(o[k], x[(size_t)rr * QUADS], wgt[rr * sp.count + i]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = tid / QUADS + k * MOST_ROWS;
+        if (rr < rows) store(rr, o[k]);
+      }
+    } else {
+      const int rr = (tid / QUADS) % rpu, grp = tid / (rpu * QUADS);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rr < rows) {
+        const float4 *x = a.part_o + (size_t)(r0 + rr) * QUADS + d4;
+#pragma unroll 4
+        for (int i = grp; i < sp.count; i += G) add(o, x[slot(i) * step], wgt[rr * sp.count + i]);
+      }
+      acc[tid] = o;
+      __syncthreads();
+      if (grp == 0 && rr < rows) {
+        for (int g = 1; g < G; ++g) add(o, acc[tid + g * rpu * QUADS], 1.f);
+        store(rr, o);
+      }
     }
     __syncthreads();
   }
@@ -1078,7 +1103,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   }
   cudaError_t e = launch_pdl(attn_kernel<D, KS>, grid, C::kThreads, C::kSmem, s, k_map, v_map, a);
   if (e == cudaSuccess)
-    e = launch_pdl(attn_join_kernel<D>, 2 * grid, JOIN_THREADS, 0, s, a, (int)grid);
+    e = launch_pdl(attn_join_kernel<D>, grid, JOIN_THREADS, 0, s, a, (int)grid);
   if (e != cudaSuccess) {
     fprintf(stderr, "mxfp4_moe: launch failed: %s\n", cudaGetErrorString(e));
     cudaGetLastError();
