@@ -519,8 +519,11 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             __syncwarp();
             const int id = __shfl_sync(FULL, page, pg);
             if (c64 < D / 64 && ((tma >> pg) & 1)) box(id);
-            if (!is_k)                                 // the other pages' rows, or zeros
-              for (int pgv = 0; pgv < boxes; ++pgv) {
+            if (!is_k) {
+              // the other pages' rows, or zeros, in the 16-row steps of the product
+              const int hull0 = max(w.q.lo - k0, 0) & ~15;
+              const int hull1 = (min(w.q.n - k0, a.tile_keys) + 15) & ~15;
+              for (int pgv = hull0 / box_rows; pgv < boxes && pgv * box_rows < hull1; ++pgv) {
                 if ((tma >> pgv) & 1) continue;
                 const bool in = (goods >> pgv) & 1;
                 const int idv = __shfl_sync(FULL, page, pgv), row0 = pgv * box_rows;
@@ -534,6 +537,8 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
                                    cache + (live ? (base + r) * D : 0) + u * 8, live);
                 }
               }
+            }
+            __syncwarp();
             cp_async_arrive_noinc(bar);
           } else {
             uint32_t idx[KT / 32];                     // rows lane + 32 c of the cache
@@ -617,10 +622,23 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           fence_proxy_async();
           tc_fence_after();
           const uint64_t vd = smem_desc(ring + vr.slot * C::kSlot, KT * 128, 1024, kSwizzle128B);
+          // the 16-key steps that hold a key of the sequence: the others weigh 0, and
+          // their values were not brought
+          auto product = [&](int c, bool first) {
+            mma_f16_ts(tm + C::kO + (WGS == 2 ? (t & 1) * D : 0),
+                       tm + C::kP + (t & 1) * (KT / 2) + c * 8, vd + c * 2048 / 16, kIdO,
+                       t >= t_first + WGS || !first);
+          };
+          if (t == t_first || t + 1 == t_end) {
+            const int k0 = w.q.start + (w.t0 + (int)(t - t_first)) * a.tile_keys;
+            const int c0 = __shfl_sync(FULL, max(w.q.lo - k0, 0) / 16, 0);
+            const int c1 = __shfl_sync(FULL, (min(w.q.n - k0, a.tile_keys) + 15) / 16, 0);
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) product(c, c == c0);
+          } else {
 #pragma unroll
-          for (int c = 0; c < KT / 16; ++c)
-            mma_f16_ts(tm + C::kO + (WGS == 2 ? (t & 1) * D : 0), tm + C::kP + (t & 1) * (KT / 2) + c * 8,
-                       vd + c * 2048 / 16, kIdO, t >= t_first + WGS || c > 0);
+            for (int c = 0; c < KT / 16; ++c) product(c, c == 0);
+          }
           mma_commit(empty + vr.slot);
           mma_commit(pv_done + (t & 1));
           vr.advance(2);
