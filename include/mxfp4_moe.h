@@ -404,7 +404,7 @@ int mxfp4_quantize(const uint16_t *w, int64_t R, int K, uint8_t *codes, uint8_t 
  *   max_pos sets MOE_DEV_BAD_INDEX and the token is left out.  Two tokens of
  *   a call must not share a place in the cache (whichever lands last stays).
  *   Limits: D 64, 128 or 256; Hq a multiple of Hkv, Hq <= 1024; 1 <= N <= 64;
- *   S*N <= 2^20; max_pages*page_size < 2^31.  bf16 tensors and cos_sin 16-byte
+ *   S*N <= 2^20; max_pages*page_size <= 2^30.  bf16 tensors and cos_sin 16-byte
  *   aligned (else MOE_ERR_INVALID_ARG).
  */
 int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, int norm,
@@ -428,8 +428,8 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
  *   for the product with v.  A token that sees no key (a slot with kv_len <=
  *   0, or a negative position) gets zeros.  Cache rows at or past kv_len, and
  *   pages that no token of the block sees, are never used, whatever they or
- *   their page ids hold.  (Rows of the block's later tokens weigh 0 for its
- *   earlier ones and, like every visible row, must be finite.)
+ *   their page ids hold; a key or value that is not finite reaches the tokens
+ *   that see it and no others.
  *   q, out      [S, N, Hq, D] bf16
  *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16
  *   block_table [S, max_pages] int32; kv_len [S] int32
@@ -493,8 +493,9 @@ int moe_get_device_status(moe_stream_t stream, int *detail);
 int moe_clear_device_status(moe_stream_t stream);
 
 /*
- * moe_set_wait_limit_ns -- time limit of the tensor-core FFN's bounded waits
- *   on the current device: 2 s by default, `ns` = 0 restores the default.
+ * moe_set_wait_limit_ns -- time limit of the bounded waits of the tensor-core
+ *   FFN and of block_attention on the current device: 2 s by default, `ns` = 0
+ *   restores the default.
  *   (The pages have no counterpart; this is the library's failure
  *   detection.)  A wait that runs past the limit ends the kernel early: it
  *   sets MOE_DEV_TIMEOUT in the device status word, waits for the copies and

@@ -44,9 +44,6 @@ namespace moe {
 constexpr int ATTN_MAX_CTAS = 148;
 constexpr int ATTN_ROWS = 128;
 constexpr int ATTN_MASKS = 8;
-#ifndef ATTN_KS64
-#define ATTN_KS64 0
-#endif
 
 struct AttnArgs {
   const uint16_t *q;                   // [S, N, Hq, D]
@@ -78,8 +75,8 @@ struct AttnSplit {
 
 template <int D, int KS>
 struct AttnCfg {
-  static constexpr int KT = D == 256 || (D == 128 && KS == ATTN_KS64) ? 64 : 128;   // keys per tile
-  static constexpr int WGS = D == 256 || KT == 128 && D == 128 ? 1 : 2;  // softmax warpgroups, a tile each in turn
+  static constexpr int KT = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int WGS = D == 64 ? 2 : 1;         // softmax warpgroups, a tile each in turn
   static constexpr int NC = KT / KS;                  // keys of a tile to one softmax thread
   static constexpr int RG = ATTN_ROWS / KS;           // rows of a lane group
   static constexpr int kSoftmax = 128 * WGS;          // softmax threads
@@ -307,10 +304,69 @@ __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// One row's sum over the keys [k0, k1) of its sequence, for rows that do not see
+// all keys of a segment whose values are not all finite: in the product with V a
+// key that the row does not see weighs 0, and 0 x NaN or infinity would be NaN.
+// A warp: lanes take a key each for the scores, then D/32 dims each for the sum.
+template <int D>
+__device__ __noinline__ void attn_row_alone(const AttnArgs &a, int s, int tok, int head, int k0,
+                                            int k1, float base, float f, uint16_t *out16,
+                                            float *out32) {
+  constexpr int W = D / 64;                              // words of two dims per lane
+  const int lane = threadIdx.x & 31, kvh = head / (a.Hq / a.Hkv);
+  const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (((size_t)s * a.N + tok) * a.Hq + head) * D);
+  float o[2 * W];
+#pragma unroll
+  for (int e = 0; e < 2 * W; ++e) o[e] = 0.f;
+  for (int b = k0; b < k1; b += 32) {
+    const int key = b + lane;
+    long long at = -1;                                   // this lane's row of the cache
+    float p = 0.f;
+    if (key < k1) {
+      const int lp = key / a.page_size;
+      const int id = __ldg(a.block_table + (size_t)s * a.max_pages + lp);
+      if (id >= 0 && id < a.num_pages)
+        at = ((long long)id * a.Hkv + kvh) * a.page_size + (key - lp * a.page_size);
+    }
+    if (at >= 0) {
+      const uint4 *k = reinterpret_cast<const uint4 *>(a.k_cache + at * D);
+      float z = 0.f;
+#pragma unroll 4
+      for (int u = 0; u < D / 8; ++u) {
+        float x[8], y[8];
+        unpack8(__ldg(q + u), x);
+        unpack8(__ldg(k + u), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z = fmaf(x[e], y[e], z);
+      }
+      p = exp2_approx(fmaf(z, a.scale_log2, -base));
+    }
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+      const float pj = __shfl_sync(FULL, p, j);
+      const long long row = __shfl_sync(FULL, at, j);
+      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v_cache + row * D) + lane * W;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const uint32_t x = row >= 0 ? __ldg(v + e) : 0u;
+        o[2 * e] = fmaf(pj, bf16_lo(x), o[2 * e]);
+        o[2 * e + 1] = fmaf(pj, bf16_hi(x), o[2 * e + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    if (out16 != nullptr)
+      reinterpret_cast<uint32_t *>(out16)[lane * W + e] = pack_bf16(o[2 * e] * f, o[2 * e + 1] * f);
+    else
+      reinterpret_cast<float2 *>(out32)[lane * W + e] = make_float2(o[2 * e], o[2 * e + 1]);
+  }
+}
+
 template <int D, int KS>
 __global__ void __launch_bounds__(AttnCfg<D, KS>::kThreads, 1)
 attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-            const AttnArgs a) {
+            const __grid_constant__ AttnArgs a) {
   typedef AttnCfg<D, KS> C;
   constexpr int KT = C::KT, WGS = C::WGS, THREADS = C::kThreads;
   constexpr int MMA_WARP = 4 * WGS, K_WARP = MMA_WARP + 1;
@@ -849,7 +905,8 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           const float2 x = ml[g * C::RG + r];
           sum += exp2_approx(x.x - base) * x.y;
         }
-        const float f = exp2_approx(m - base) * (whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float f = exp2_approx(m - base) * (whole ? inv : 1.f);
         if (!whole && live && wg == 0 && kq == 0)
           a.part_ml[(size_t)slot * a.rows_cap + r] = make_float2(top, sum);
         softmax_sync<C::kSoftmax>();
@@ -857,6 +914,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
         float4 *const piece = a.part_o + (size_t)slot * a.rows_cap * (D / 4) + (tid & 7);
         const int rows = min(C::RG, a.rows - w.rb * ATTN_ROWS);
         const uint32_t ot = lanes + C::kO + (uint32_t)wg * D;
+        bool finite = true;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           if (warp_live) {
@@ -881,11 +939,29 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
               const float4 y = from[g * C::RG];
               x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
             }
+            finite = finite && fmaf(x.x, 0.f, fmaf(x.y, 0.f, fmaf(x.z, 0.f, x.w * 0.f))) == 0.f;
             if (whole)
               *reinterpret_cast<uint2 *>(item + row_at[rr] + c * 32) =
                   make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
             else
               piece[(size_t)rr * (D / 4) + c * 8] = x;
+          }
+          if (c + 1 < D / 32) softmax_sync<C::kSoftmax>();
+        }
+        if (!softmax_all<C::kSoftmax>(finite)) {
+          // values that are not finite: the rows that do not see all of the segment's
+          // keys are summed anew over those that they see
+          if (wg == 0 && kq == 0) ml[r] = make_float2(base, inv);
+          softmax_sync<C::kSoftmax>();
+          const int ka = max(w.q.lo, w.q.start + w.t0 * a.tile_keys);
+          const int kb = (int)min((long long)w.q.n, w.q.start + (long long)w.t1 * a.tile_keys);
+          for (int rr = warp; rr < rows; rr += C::kSoftmax / 32) {
+            const int at = w.rb * ATTN_ROWS + rr, i = at / group, p = w.q.n - a.N + i;
+            const int k0 = max(ka, a.window > 0 ? p - a.window + 1 : 0), k1 = min(kb, p + 1);
+            if (k0 == ka && k1 == kb) continue;
+            attn_row_alone<D>(a, w.s, i, w.kvh * group + at - i * group, k0, k1, ml[rr].x, ml[rr].y,
+                              whole ? item - (tid & 7) * 4 + row_at[rr] : nullptr,
+                              reinterpret_cast<float *>(piece - (tid & 7) + (size_t)rr * (D / 4)));
           }
           softmax_sync<C::kSoftmax>();
         }

@@ -59,6 +59,8 @@ __device__ __forceinline__ bool offsets_ok(const int32_t *off, int E, long P) {
 constexpr unsigned FULL = 0xffffffffu;
 
 constexpr int BLOCK_MAX_TOKENS = 64;   // tokens per sequence of a drafted block
+// Positions of a sequence: sums of a length, a window and a tile stay in an int.
+constexpr int BLOCK_MAX_LENGTH = 1 << 30;
 
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialisation, so the next kernel on the stream

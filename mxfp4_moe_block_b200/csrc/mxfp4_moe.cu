@@ -492,7 +492,7 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
   if (rot < 0 || rot > D || rot % 16 || (rot && (!cos_sin || max_pos < 1)) || max_pages < 1 ||
       num_pages < 1 || page_size < 1 || (norm && !(eps >= 0.f)))
     return MOE_ERR_INVALID_ARG;
-  if ((long long)max_pages * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page_size > BLOCK_MAX_LENGTH) return MOE_ERR_UNSUPPORTED;
   if (S == 0) return MOE_OK;
   if (!qkv || !kv_len || !block_table || !k_cache || !v_cache || !q_out) return MOE_ERR_INVALID_ARG;
   if (misaligned16(qkv) || misaligned16(q_weight) || misaligned16(k_weight) ||
@@ -523,7 +523,7 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
   if (st != MOE_OK) return st;
   if (max_pages < 1 || num_pages < 1 || page_size < 1 || window < 0 || !(scale >= 0.f && scale < INFINITY))
     return MOE_ERR_INVALID_ARG;
-  if ((long long)max_pages * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page_size > BLOCK_MAX_LENGTH) return MOE_ERR_UNSUPPORTED;
   if (S == 0) return MOE_OK;
   if (!q || !k_cache || !v_cache || !block_table || !kv_len || !out || !workspace)
     return MOE_ERR_INVALID_ARG;
@@ -544,7 +544,7 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
   a.block_table = block_table, a.max_pages = max_pages;
   a.kv_len = kv_len;
   a.scale_log2 = fmaxf(scale * 1.44269504f, FLT_MIN);
-  a.window = window;
+  a.window = window >= BLOCK_MAX_LENGTH ? 0 : window;   // (no position that it cuts off)
   a.out = out;
   uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
   const cudaStream_t cs = (cudaStream_t)stream;

@@ -298,11 +298,150 @@ def test_attention_pages_before_the_window_are_not_used():
     check_attention(st, window, mm.block_attention(**to_dev(st), window=window))
 
 
+@pytest.mark.parametrize("c", [
+    (3, 8, 8, 4, 64, 16, [900, 7, 128], 100), (2, 8, 16, 2, 128, 16, [600, 1030], 0),
+    (2, 16, 16, 2, 128, 24, [400, 1500], 200), (2, 33, 14, 2, 128, 64, [33, 260], 40),
+    (4, 5, 6, 2, 256, 16, [64, 195, 1000, 6], 70), (1, 64, 32, 1, 64, 128, [500], 65)], ids=str)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attention_values_that_are_not_finite_reach_no_other_token(c, value):
+    """The last token's value, and that of the first key in the window: of the
+    block's tokens only the last, only the first, sees it."""
+    S, N, Hq, Hkv, D, page, lens, window = c
+    st, _ = attention_case(c, 65)
+    d = to_dev(st)
+    for s, n in enumerate(lens):
+        marks = [n - 1] + ([n - N - window + 1] if window and n - N - window >= 0 else [])
+        for j in marks:
+            d["v_cache"][st["block_table"][s, j // page], :, j % page, 5:D:7] = value
+    out = mm.block_attention(**d, window=window)
+    for s, n in enumerate(lens):
+        seeing = [N - 1] + ([0] if window and n - N - window >= 0 else [])
+        for i in seeing:
+            assert not torch.isfinite(out[s, i, :, 5]).any()
+            assert torch.isfinite(out[s, i, :, 4]).all()
+            # (their other dims hold what the oracle has; these are set to it)
+            want = oatt.attention(f64(st["q"])[s:s + 1], f64(st["k_cache"]), f64(st["v_cache"]),
+                                  st["block_table"].numpy()[s:s + 1], st["kv_len"].numpy()[s:s + 1],
+                                  None, window)[0]
+            out[s, i, :, 5:D:7] = torch.from_numpy(want[0, i, :, 5:D:7]).to(out)
+    check_attention(st, window, out)
+
+
 def test_attention_shared_pages():
     """Two sequences share a prefix's pages."""
     st, window = attention_case((2, 2, 8, 2, 128, 16, [90, 90], 0), 63)
     st["block_table"][1, :4] = st["block_table"][0, :4]
     check_attention(st, window, mm.block_attention(**to_dev(st)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [40, 48, 200, 256, 384, 512])
+def test_attention_page_sizes(D, page):
+    """Pages smaller and larger than a tile, multiples of it and not, whole and
+    seen in part at both ends."""
+    for window in (0, 300):
+        st, window = attention_case((3, 3, 6, 2, D, page, [1500, 511, 2 * page + 1], window), page + window)
+        check_attention(st, window, mm.block_attention(**to_dev(st), window=window))
+
+
+def test_attention_many_rows_and_splits():
+    """512 rows to a key/value head (four blocks of rows), cut among the GPU."""
+    st, window = attention_case((2, 64, 16, 2, 64, 16, [2000, 300], 0), 67)
+    check_attention(st, window, mm.block_attention(**to_dev(st)))
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (128, 5), (256, 64)])
+def test_attention_bad_pages_in_the_window(D, page):
+    st, window = attention_case((4, 6, 4, 2, D, page, [700, 90, 300, 1000], 250), 69)
+    for k in ("k_cache", "v_cache"):
+        st[k] = torch.nan_to_num(st[k])
+    for s, n in enumerate([700, 90, 300, 1000]):
+        st["block_table"][s, (n - 1) // page - s] = st["k_cache"].shape[0] + s
+        st["block_table"][s, max(0, n - 200) // page] = -1
+    check_attention(st, window, mm.block_attention(**to_dev(st), window=window))
+
+
+@pytest.mark.parametrize("page,D", [(1 << 16, 64), (1 << 14, 256), (24, 128)])
+def test_attention_positions_near_the_limit(page, D):
+    """Lengths just below 2^30 behind a window, and a window past every position."""
+    pages = (1 << 30) // page
+    N, window, n = 9, 130, pages * page - 3
+    g = torch.Generator().manual_seed(70)
+    st = dict(q=bf16((2, N, 4, D), 1, 2.0), k_cache=bf16((4, 2, page, D), 2),
+              v_cache=bf16((4, 2, page, D), 3), kv_len=i32([n, 5]),
+              block_table=torch.randint(0, 4, (2, pages), generator=g, dtype=torch.int32))
+    check_attention(st, window, mm.block_attention(**to_dev(st), window=window))
+    st["kv_len"] = i32([70, 5])
+    for big in ((1 << 31) - 1, 1 << 30):
+        check_attention(st, big, mm.block_attention(**to_dev(st), window=big))
+
+
+@pytest.mark.parametrize("page", [16, 24])
+def test_cache_offsets_past_32_bits(page):
+    """Pages at the far end of caches of more than 2^32 elements: append, then
+    attend."""
+    S, N, Hq, Hkv, D, n = 2, 4, 8, 8, 128, 300
+    pages = (1 << 32) // (Hkv * page * D) + 60
+    kc, vc = (torch.empty((pages, Hkv, page, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    need = -(-n // page)
+    table = pages - 1 - torch.arange(S * need, dtype=torch.int32).reshape(S, need)
+    first = pages - S * need
+    for t, seed in ((kc, 5), (vc, 6)):
+        t[first:] = bf16((S * need, Hkv, page, D), seed).to(DEV)
+    qkv, kv_len = bf16((S, N, Hq + 2 * Hkv, D), 7), i32([n, n - 1])
+    q = mm.block_kv_append(qkv.to(DEV), kv_len.to(DEV), table.to(DEV), kc, vc, norm=False)
+    out = mm.block_attention(q, kc, vc, table.to(DEV), kv_len.to(DEV))
+    st = dict(q=qkv[:, :, :Hq], k_cache=kc[first:].cpu(), v_cache=vc[first:].cpu(),
+              block_table=table - first, kv_len=kv_len)
+    assert torch.equal(q.cpu(), st["q"])
+    for s in range(S):
+        for i in range(N):
+            p = int(kv_len[s]) - N + i
+            row = st["k_cache"][st["block_table"][s, p // page], :, p % page]
+            assert torch.equal(row, qkv[s, i, Hq:Hq + Hkv])
+    check_attention(st, 0, out)
+
+
+def test_attention_two_calls_at_once():
+    """Two streams, a workspace each, many calls in flight."""
+    cases = [attention_case((6, 8, 16, 2, 128, 16, [1500, 20, 900, 0, 8, 400], 0), 72)[0],
+             attention_case((3, 3, 8, 4, 64, 24, [700, 2000, 33], 0), 73)[0]]
+    dev = [to_dev(c) for c in cases]
+    outs = [[torch.empty_like(d["q"]) for _ in range(6)] for d in dev]
+    streams = [torch.cuda.Stream() for _ in dev]
+    ws = [mm.alloc_attention_workspace(*d["q"].shape[:3], d["k_cache"].shape[1], d["q"].shape[3], DEV) for d in dev]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for d, o, st, w in zip(dev, outs, streams, ws):
+            mm.block_attention(**d, out=o[i], workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        check_attention(c, 0, o[0])
+        assert all(torch.equal(o[0], x) for x in o[1:])
+
+
+@pytest.mark.parametrize("c", [(40, 2, 16, 8, 128, 16, [600, 250], 0), (40, 8, 48, 8, 128, 16, [600, 250], 0),
+                               (40, 16, 64, 8, 64, 24, [600, 250], 0), (40, 5, 16, 8, 256, 16, [600, 250], 0)], ids=str)
+def test_attention_wait_runs_out_and_the_next_call_is_right(c):
+    """A limit far below a wait's time: MOE_DEV_TIMEOUT is reported, the copies
+    and products in flight are waited for, the next call is right.  The long
+    wait: each CTA has several sequences, and a last value that is not finite
+    has a sequence's earlier rows summed anew, key by key, meanwhile the next
+    sequence's weights are waited for."""
+    c = c[:6] + ((c[6] * 20),) + c[7:]
+    st, window = attention_case(c, 74)
+    d = to_dev(st)
+    v = d["v_cache"].clone()
+    for s, n in enumerate(c[6]):
+        v[st["block_table"][s, (n - 1) // c[5]], :, (n - 1) % c[5]] = float("nan")
+    try:
+        mm.moe_set_wait_limit_ns(1)
+        mm.block_attention(**{**d, "v_cache": v}, window=window)
+        assert mm.moe_get_device_status() == (5, 4)
+    finally:
+        mm.moe_set_wait_limit_ns(0)
+        mm.moe_clear_device_status()
+    check_attention(st, window, mm.block_attention(**d, window=window))
 
 
 def test_attention_same_bits_again_and_on_another_stream():
@@ -401,6 +540,54 @@ def test_sample_rows_without_mass():
     z[1, 0] = float("nan")
     check_sample(z, uniforms((2, 2), 1), top_k=i32([5, 0]), top_p=torch.tensor([0.5, 0.5]))
     assert mm.moe_get_device_status() == NO_MASS
+
+
+@pytest.mark.parametrize("k", [127, 128, 129, 2000, 2048, 2049, 6000])
+def test_sample_top_k_sizes(k):
+    """Around the sizes where the selection changes its way, without ties, with
+    some and with thousands at the border."""
+    V = 20011
+    z = torch.randn((1, 3, V), generator=torch.Generator().manual_seed(k)) * 2
+    z[:, 1] = z[:, 1].to(torch.bfloat16).float()
+    z[:, 2] = z[:, 2].round()
+    for f in (dict(top_k=i32([k])), dict(top_k=i32([k]), top_p=torch.tensor([0.7])),
+              dict(top_k=i32([k]), top_p=torch.tensor([0.9]), min_p=torch.tensor([0.02]))):
+        check_sample(z, uniforms((1, 3), k), **f)
+
+
+def test_sample_largest_vocabulary_and_heavy_ties():
+    V = 393216
+    z = torch.randn((1, 3, V), generator=torch.Generator().manual_seed(12)) * 2
+    z[:, 1] = z[:, 1].round()
+    z[:, 2] = 0.0
+    for f in ({}, dict(top_p=torch.tensor([0.9])), dict(min_p=torch.tensor([0.3])),
+              dict(top_k=i32([100000]), top_p=torch.tensor([0.6]))):
+        check_sample(z, uniforms((1, 3), 13), **f)
+
+
+def test_sample_many_rows():
+    """More rows than one launch's grid takes."""
+    S, K, V = 23000, 3, 9
+    z = torch.randn((S, K, V), generator=torch.Generator().manual_seed(14))
+    u = uniforms((S, K), 15)
+    token, probs = mm.block_sample(z.to(DEV), u.to(DEV), with_probs=True)
+    z64 = z.double().numpy()
+    w = np.exp(z64 - z64.max(-1, keepdims=True))
+    W = np.floor(w * 2.0 ** 40)
+    m = np.floor(W.sum(-1) * u.double().numpy())
+    want = (np.cumsum(W, -1) > m[..., None]).argmax(-1)
+    p = w / w.sum(-1, keepdims=True)
+    assert (abs(f64(probs) - p) <= 2.0 ** -22 * p).all()
+    # (numpy's exponential may differ in the last unit of 2^40: a draw on the border)
+    border = (abs(np.cumsum(W, -1) - m[..., None]) <= V).any(-1)
+    assert np.array_equal(token.cpu().numpy()[~border], want[~border]) and border.mean() < 1e-6
+
+
+def test_sample_extreme_temperatures():
+    z = torch.randn((6, 2, 3001), generator=torch.Generator().manual_seed(16)) * 2
+    t = torch.tensor([1e-30, 1e30, 1e-42, math.inf, 3.4e38, 1e-3])
+    check_sample(z, uniforms((6, 2), 17), temperature=t)
+    check_sample(z, uniforms((6, 2), 18), temperature=t, top_p=torch.full((6,), 0.8), top_k=i32([9] * 6))
 
 
 def test_sample_exact_borders():

@@ -150,7 +150,8 @@ def sample(L, **kw):
     (dict(max_pages=1 << 20, ps=1 << 12), 2), (dict(qkv=None), 1), (dict(kv_len=None), 1),
     (dict(table=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(q_out=None), 1),
     (dict(qkv=A + 2), 1), (dict(k=A + 8), 1), (dict(v=A + 2), 1), (dict(q_out=A + 4), 1),
-    (dict(cs=A + 4), 1), (dict(qw=A + 2), 1), (dict(kw=A + 2), 1), (dict(S=0, qkv=None), 0)])
+    (dict(cs=A + 4), 1), (dict(qw=A + 2), 1), (dict(kw=A + 2), 1), (dict(S=0, qkv=None), 0),
+    (dict(max_pages=(1 << 18) + 1, ps=1 << 12), 2), (dict(max_pages=1 << 18, ps=1 << 12, qkv=None), 1)])
 def test_append_refusals(library, kw, status):
     assert append(library, **kw) == status
 
@@ -162,7 +163,8 @@ def test_append_refusals(library, kw, status):
     (dict(max_pages=1 << 20, ps=1 << 12), 2), (dict(q=None), 1), (dict(k=None), 1),
     (dict(v=None), 1), (dict(table=None), 1), (dict(kv_len=None), 1), (dict(out=None), 1),
     (dict(ws=None), 1), (dict(ws_bytes=16), 4), (dict(ws=A + 16), 4), (dict(q=A + 2), 1),
-    (dict(k=A + 8), 1), (dict(v=A + 8), 1), (dict(out=A + 2), 1), (dict(S=0, q=None), 0)])
+    (dict(k=A + 8), 1), (dict(v=A + 8), 1), (dict(out=A + 2), 1), (dict(S=0, q=None), 0),
+    (dict(max_pages=(1 << 18) + 1, ps=1 << 12), 2), (dict(max_pages=1 << 18, ps=1 << 12, q=None), 1)])
 def test_attention_refusals(library, kw, status):
     assert attention(library, **kw) == status
 
