@@ -467,14 +467,16 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
  *     token = least kept v whose sum of kept W up to v exceeds
  *             floor(sum of kept W * U / 2^24), U = u * 2^24.
  *   The first-ranked token is always kept.  temperature <= 0 (or NaN): the
- *   first-ranked token with probability 1.  top_k <= 0 or >= V, top_p >= 1 (or
+ *   first-ranked token with probability 1; others count as at least 1e-36 and at
+ *   most 1e30.  top_k <= 0 or >= V, top_p >= 1 (or
  *   NaN), min_p <= 0 (or NaN) switch a filter off; min_p > 1 counts as 1.
  *   Logits of -infinity (masked tokens) have weight 0, NaN counts as
  *   -infinity, +infinity takes all mass; a row with no logit above -infinity
  *   sets MOE_DEV_NO_MASS: token -1, probs 0.
  *   logits [S, K, V] float; temperature, top_p, min_p [S] float, top_k [S]
  *   int32 (a sequence's setting holds for its K rows), each NULL for off;
- *   u [S, K] float uniforms in [0,1), multiples of 2^-24; token [S, K] int32
+ *   u [S, K] float uniforms in [0,1), multiples of 2^-24 (below 0 counts as 0, 1
+ *   and above as the last step, NaN likewise); token [S, K] int32
  *   out (u and token both given or both NULL); probs [S, K, V] float out or
  *   NULL, must not overlap logits.
  *   Limits: 1 <= K <= 64, 1 <= V <= 393216, S*K <= 2^20.

@@ -4,17 +4,20 @@
 //
 // The N tokens x (Hq/Hkv) query heads that share a key/value head are the rows
 // of one matrix: S = Q K^T and O += P V run on tcgen05 with 128 rows (rows past
-// the last are zeros), keys in tiles of KT, S and O in tensor memory.  At
-// these row counts the cache's bytes bound the call (2 flops per row and byte
-// against ~250 flops per byte of the machine), so a padded 128-row MMA costs
-// nothing: a 64 KB tile (128 keys, D = 128) takes the tensor pipe ~1000 cycles
-// and an SM's share of HBM ~2700.
+// the last are left as they are, and reach no output), keys in tiles of KT = 128
+// (64 for D = 256, whose queries take twice the shared memory), S, P and O in
+// tensor memory.  At these row counts the cache's bytes bound the call (2 flops
+// per row and byte against ~250 flops per byte of the machine), so a padded
+// 128-row MMA costs nothing: a 64 KB tile (128 keys, D = 128) takes the tensor
+// pipe ~1000 cycles and an SM's share of HBM ~2700.
 //
 // Softmax in one pass: every row keeps a maximum m and a sum l in float; O is
 // rescaled only when a tile's maximum exceeds m by 8 (in powers of two), so
 // weights reach 2^8 at most and the accumulator in tensor memory is rarely
-// touched.  The weights go to the tensor cores as bf16 (8 bits, half a step
-// 2^-9 of a weight, like the keys and values); l sums them before rounding.
+// touched.  The weights go to the tensor cores as bf16, which its product with
+// the bf16 values asks for (half a step, 2^-8 of a weight, like the keys and
+// values); l sums them before rounding.  Values that are not finite would spoil
+// the rows that do not see them (0 x NaN): see attn_row_alone.
 //
 // Split over the length: the tiles of all (sequence, key/value head, row block)
 // items form one line, cut into G equal pieces, one per CTA (one CTA per SM),
@@ -23,16 +26,30 @@
 // its unnormalised O, m and l in the workspace and attn_join_kernel adds them
 // in the order of the pieces (the same bits on every run).
 //
-// Warps: 0-3 softmax (a thread per row, tensor-memory lane = row; they also
-// bring the queries), 4 the MMA issuer, 5 and 6 the producers of the K and the V
-// tiles of a shared ring in the 128-byte swizzle: by TMA page by page, or row by
-// row through cp.async, where rows outside the sequence or on a bad page are
-// zero-filled and masked by a bit per key.
+// Warps: a warpgroup of softmax threads (a thread per row, tensor-memory lane =
+// row; they also bring the queries), the MMA issuer, and the producers of the K
+// and the V tiles of a shared ring in the 128-byte swizzle: by TMA page by page
+// where pages are multiples of 8 rows, or row by row through cp.async, where rows
+// outside the sequence or on a bad page are zero-filled and masked by a bit per
+// key.  (By rows alone: 16 sequences of up to 30000 keys 246 us, by TMA 156.)  The
+// ring's order is that of use, K0 K1 V0 K2 V1 .., each tile scored two ahead of
+// its product with V.  For D = 64 a tile's bytes arrive in half the time, but its
+// weights take as long: two warpgroups take every other tile, each with an O of
+// its own (64 sequences of 5000 keys, 16 heads, 8 tokens: 256 us, with one 281).
 //
 // Few rows would leave most lanes, and so most softmax warps, without work: up
 // to 32 rows (64) the queries stand in the 128 MMA rows four (two) times, lane
 // group g weighs the g-th quarter (half) of each tile's keys, its other weights
-// stay zero, and the groups' O, m and l are joined at the segment's end.
+// stay zero, and the groups' O, m and l are joined at the segment's end.  (64
+// sequences, 16 heads of 64, window: 37 us, without groups 51, with two 41; a
+// sequence of 131000 keys, 8 rows to a head: 58 us, without 61.)
+//
+// Measured (floor: the visible cache once at a plain copy's rate): 16 sequences of
+// up to 30000 keys, 64/8 heads of 128, 8 tokens 156 us (132); 64 of up to 9000,
+// 32/4 heads, 16 tokens 142 us (98); one of 131000, 32/4 heads, one token 58 us
+// (41); one of 777 keys 14 us (0.5).  What is left: the start of a call (barriers,
+// tensor memory, the pieces' places, the first tiles) 4-5 us, the join 4-6 us, the
+// output of an item 1.3 us, in which its CTA's loads run on into the ring only.
 // Every wait is bounded (MOE_DEV_TIMEOUT), as in the expert FFN.
 #pragma once
 #include "common.cuh"
@@ -239,6 +256,8 @@ struct AttnRing {
   }
 };
 
+// What an item costs beside its tiles, in tiles (the walk below; 64 sequences of up
+// to 9000 keys, 4 heads: 142 us with 3, 156 with 0; a single sequence is the same).
 constexpr unsigned ATTN_ITEM_COST = 3;
 __device__ __forceinline__ unsigned attn_cost(int tiles) {
   return tiles ? (unsigned)tiles + ATTN_ITEM_COST : 0;
@@ -1206,7 +1225,7 @@ inline int attn_launch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   return MOE_OK;
 }
 
-// Lane groups by the rows to a key/value head (see the kernel's head).
+// Lane groups by the rows to a key/value head (measured at the head of this file).
 template <int D>
 inline int attn_dispatch(AttnArgs a, uint8_t *ws, int sms, cudaStream_t s) {
   a.rows = a.N * (a.Hq / a.Hkv);

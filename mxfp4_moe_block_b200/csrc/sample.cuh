@@ -15,19 +15,27 @@
 // shared memory once and every later pass reads it there.  The threshold is
 // found without sorting the row: a histogram of the distance to the maximum
 // (counts, and exact masses where top-p needs them) over 1024 buckets names the
-// bucket of the threshold; its few tokens -- and, for a small top-k, all
-// tokens above -- go to the cluster's first CTA, which sorts them.  A bucket
-// with more tokens than that list holds (many nearly equal logits) is split
-// again by the bits of the logit, three times at most, and a group of equal
-// logits is cut by a quotient and a count.
+// bucket of the threshold, whose few tokens go to the cluster's first CTA; with
+// four words (logit, ~index) to a thread it narrows them by histograms of its own
+// and ranks the last 32 by comparing.  A bucket with more tokens than that list
+// holds (many nearly equal logits) is split again by the bits of the logit, three
+// times at most, and a group of equal logits is cut by a quotient and a count.  A
+// small top-k needs no histogram over the cluster: the k first-ranked lie above
+// the k-th largest of a CTA's 512 threads' own maxima, and the first CTA settles
+// the row from the tokens there.
 //
-// The exponentials are the arithmetic: an SM does 64 double operations a cycle
-// and a weight with its mass takes 13, ~5 weights per cycle and SM, against ~6
-// logits per cycle that HBM delivers to an SM (and as many probabilities taken
-// back).  So each kept token's weight is
-// computed once (twice for top-p over a whole row), the float of it stays in
-// shared memory for the probabilities, and the draw recomputes 1/16 of one
-// slice.
+// Bounds.  The bytes: a row in and, where wanted, its probabilities out.  The
+// exponentials: an SM does 64 double operations a cycle and a weight with its mass
+// takes 12 (and two conversions, 16 a cycle), ~5 weights per cycle and SM, against
+// ~6 logits per cycle that HBM delivers to an SM.  So a kept token's weight is
+// computed once (top-p over a whole row: every weight, and the kept ones again);
+// where few are kept (top-k, top-p) they wait in a queue until a warp has 32 of
+// them; the float of a weight stays in shared memory for the probabilities.  And
+// the row's steps one after another: five to nine barriers of the cluster and the
+// first CTA's search between them, ~11 us for a row of 32000, hidden by other rows
+// only as far as two CTAs fit an SM.  Measured: one row of 32000 (top-k 50, top-p
+// and min-p) 14 us; 128 rows of 152064 with mixed filters, tokens only, 139 us
+// (24 us at HBM's rate); 1024 rows of 32000 with probabilities 109 us (40 us).
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -74,14 +82,12 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // comes from float (it need not be exact: the remainder f is), 2^f on
 // [-1/2, 1/2] is 1 + f p(f), p of degree 7 fitted to the least relative error
 // at Chebyshev nodes: 2^-40, the masses' own step.  11 double operations and
-// two conversions.  Temperatures below 1e-36 count as 1e-36, so that the scale
-// stays finite in float.
+// two conversions.
 struct SampleScale {
   double top, c;
   float ftop, fc, below;          // weights of x - top <= below are 0
   __device__ __forceinline__ SampleScale(float t, double scale)
-      : top((double)t), c(fmin(scale, 1e36)), ftop(t), fc((float)c),
-        below(fmaxf((float)(-1000.0 / c), -FLT_MAX)) {}
+      : top((double)t), c(scale), ftop(t), fc((float)c), below((float)(-1000.0 / c)) {}
   __device__ __forceinline__ bool positive(float x) const { return x - ftop > below; }   // NaN: no
   __device__ __forceinline__ double weight(float x) const {
     const float magic = 12582912.f + 40.f;                          // 1.5 2^23, and the 2^40
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const int k = a.top_k ? __ldg(a.top_k + s) : 0;
   const double p = a.top_p ? (double)__ldg(a.top_p + s) : 1.0;
   const float mp = a.min_p ? __ldg(a.min_p + s) : 0.f;
-  const u64 U = a.token ? (u64)((double)__ldg(a.u + row) * 16777216.0) : 0;
+  const u64 U = a.token ? (u64)(fminf(__ldg(a.u + row), 0x0.ffffffp0f) * 16777216.f) : 0;   // < 2^24
   asm volatile("cp.async.wait_all;" ::: "memory");
   // (each thread reads back what it copied itself)
   float most = -INFINITY;
@@ -311,7 +317,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       });
     return;                                       // (no remote access after the exchange)
   }
-  const SampleScale z(top, 1.4426950408889634 / T);
+  // (limits that keep the scale, its reciprocal and its products finite in float)
+  const SampleScale z(top, 1.4426950408889634 / fmin(fmax(T, 1e-36), 1e30));
   auto mass_at = [&](float l) -> u64 { return z.positive(l) ? sample_mass(z.weight(l)) : 0; };
 
   // ---- the threshold: kept are logits above `at`, and at it the tokens <= last ----
@@ -947,7 +954,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 }
 
 // CTAs of a row: slices of at most 18432 tokens (72 KB, two CTAs per SM) and,
-// for few rows, enough CTAs for the machine with 2048 tokens each at least.
+// for few rows, enough CTAs for the machine with 2048 tokens each at least.  (1024
+// rows of 32000: two CTAs 110 us, one 129, four 156, the steps between barriers
+// being paid by each; a single row of 32000: eight CTAs 14.0 us, two 15.0.)
 inline int sample_cluster(int rows, int V, int sms) {
   int c = 1;
   while (c < SAMPLE_MAX_CLUSTER &&

@@ -25,8 +25,9 @@ def kept_tokens(l: np.ndarray, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         w = np.zeros(len(l))
         w[rank[0]] = 1.0
         return rank[:1], w, [ONE if v == rank[0] else 0 for v in range(len(l))]
+    temperature = min(max(float(temperature), 1e-36), 1e30)
     with np.errstate(invalid="ignore", over="ignore"):
-        w = np.where(l == top, 1.0, np.exp((l - top) / float(temperature)))
+        w = np.where(l == top, 1.0, np.exp((l - top) / temperature))
     W = [int(math.floor(x * ONE)) for x in w]
     n = top_k if 0 < top_k < len(l) else len(l)
     rank = rank[:n]

@@ -588,6 +588,18 @@ def test_sample_extreme_temperatures():
     t = torch.tensor([1e-30, 1e30, 1e-42, math.inf, 3.4e38, 1e-3])
     check_sample(z, uniforms((6, 2), 17), temperature=t)
     check_sample(z, uniforms((6, 2), 18), temperature=t, top_p=torch.full((6,), 0.8), top_k=i32([9] * 6))
+    z[:, :, ::5] = torch.finfo(torch.float32).min          # masked: no weight at any temperature
+    check_sample(z, uniforms((6, 2), 19), temperature=t)
+
+
+def test_sample_uniforms_outside_their_range():
+    """They count as the nearest one inside: a token is always drawn."""
+    z = torch.randn((4, 1, 500), generator=torch.Generator().manual_seed(20)) * 2
+    u = torch.tensor([[1.0], [7.5], [-0.25], [float("nan")]])
+    token, _ = mm.block_sample(z.to(DEV), u.to(DEV), top_k=i32([0, 30, 30, 0]).to(DEV))
+    inside = torch.tensor([[1 - 2.0 ** -24], [1 - 2.0 ** -24], [0.0], [1 - 2.0 ** -24]])
+    want, _ = osam.block_sample(z.double().numpy(), inside.numpy(), top_k=np.array([0, 30, 30, 0]))
+    assert np.array_equal(token.cpu().numpy(), want)
 
 
 def test_sample_exact_borders():
