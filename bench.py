@@ -10,7 +10,8 @@ over a 152064-token vocabulary).  Metric: verified tokens/s (= S*K / step
 time), with the expert FFN's roofline beside it.  On one GPU the same line
 carries `per_config`: the other seeded workloads (tiny, serving batch, DFlash
 block-16 with rejection acceptance, the 8-layer stack) each timed the same
-way with its own roofline, plus the MXFP4 weight quantiser.
+way with its own roofline, plus the MXFP4 weight quantiser and the rest of a
+serving block's step: cache append, attention, sampling.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
                     [--workload NAME] [--no-per-config] [--no-cpu-baseline]
@@ -62,7 +63,8 @@ def parse(argv=None):
     ap.add_argument("--no-per-config", action="store_true")
     ap.add_argument("--per-config", default=",".join(PER_CONFIG),
                     help="comma-separated workloads for the per_config object (the "
-                         "quantiser is always measured; 'none' for it alone)")
+                         "quantiser and the block's cache append, attention and sampling "
+                         "are always measured; 'none' for them alone)")
     ap.add_argument("--experts", type=int, default=0,
                     help="override the expert count (smaller cases for profiler captures)")
     return ap.parse_args(argv)
@@ -734,6 +736,78 @@ def measure_quantize(device, peaks, reps=10):
                                                    "dram_bytes_per_launch")}}
 
 
+# ------------------------------------- cache append, attention and sampling --
+
+def measure_block(device, peaks, reps=10):
+    """block_kv_append, block_attention and block_sample as one serving step runs
+    them (16 sequences x 8 tokens, 64/8 heads of 128, caches of up to 30000 tokens
+    in pages of 32, a 152064-token vocabulary; a new set of inputs each step, three
+    in turn, larger than L2), captured and timed one by one and as a step."""
+    import mxfp4_moe_block_b200 as mm
+    S, N, Hq, Hkv, D, page, V, sets = 16, 8, 64, 8, 128, 32, 152064, 3
+    g = torch.Generator(device=device)
+    g.manual_seed(4321)
+    normal = lambda *shape: torch.randn(shape, generator=g, device=device)
+    lens = torch.linspace(500, 30000, S).int().tolist()
+    need = [-(-n // page) for n in lens]
+    kv_len = torch.tensor(lens, dtype=torch.int32, device=device)
+    table = torch.full((S, max(need)), -1, dtype=torch.int32, device=device)
+    ids = torch.randperm(sum(need), generator=g, device=device).int()
+    for s in range(S):
+        table[s, :need[s]] = ids[sum(need[:s]):sum(need[:s + 1])]
+    angle = torch.arange(30000, device=device)[:, None] * 1e4 ** (-torch.arange(D // 2, device=device) / (D // 2))
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float().contiguous()
+    st = [dict(qkv=normal(S, N, Hq + 2 * Hkv, D).bfloat16(), logits=normal(S, N, V) * 2,
+               k=normal(sum(need), Hkv, page, D).bfloat16(), v=normal(sum(need), Hkv, page, D).bfloat16(),
+               u=torch.randint(0, 1 << 24, (S, N), generator=g, device=device).float() * 2.0 ** -24,
+               q=torch.empty((S, N, Hq, D), dtype=torch.bfloat16, device=device),
+               out=torch.empty((S, N, Hq, D), dtype=torch.bfloat16, device=device),
+               token=torch.empty((S, N), dtype=torch.int32, device=device),
+               probs=torch.empty((S, N, V), device=device)) for _ in range(sets)]
+    ws = mm.alloc_attention_workspace(S, N, Hq, Hkv, D, device)
+    temp = torch.full((S,), 0.8, device=device)
+    top_k = torch.full((S,), 50, dtype=torch.int32, device=device)
+    top_p = torch.full((S,), 0.95, device=device)
+    append = lambda t: mm.block_kv_append(t["qkv"], kv_len, table, t["k"], t["v"], cos_sin=cos_sin, q_out=t["q"])
+    attend = lambda t: mm.block_attention(t["q"], t["k"], t["v"], table, kv_len, out=t["out"], workspace=ws)
+    sample = lambda t: mm.block_sample(t["logits"], t["u"], temperature=temp, top_k=top_k, top_p=top_p,
+                                       token=t["token"], probs=t["probs"])
+
+    def timed(*calls):
+        for t in st:                                   # (first calls set attributes: outside a capture)
+            for f in calls:
+                f(t)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for t in st:
+                for f in calls:
+                    f(t)
+        for _ in range(3):
+            graph.replay()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(reps):
+            graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / (reps * sets)
+
+    byts = {"append": 2 * S * N * (Hq + 2 * Hkv) * D * 2 + S * N * D * 4,
+            "attention": 2 * sum(lens) * Hkv * D * 2 + 2 * S * N * Hq * D * 2,
+            "sample": 2 * S * N * V * 4}
+    res = {"shape": {"S": S, "N": N, "heads": [Hq, Hkv, D], "page": page, "cache": [lens[0], lens[-1]], "V": V}}
+    for name, f in (("append", append), ("attention", attend), ("sample", sample)):
+        ms = timed(f)
+        gbs = byts[name] / (ms * 1e-3) / 1e9
+        res[name] = {"ms": ms, "roofline": {
+            "bound": "hbm", "achieved": gbs, "peak": peaks["hbm_gbs"], "unit": "GB/s",
+            "frac": gbs / peaks["hbm_gbs"], "algorithmic_bytes": byts[name]}}
+    res["ms"] = timed(append, attend, sample)
+    assert mm.moe_get_device_status()[0] == 0
+    return res
+
+
 # --------------------------------------------------------------- per config --
 
 def measure_config(name, variant, steps, warmup, device, peaks, clocks, with_cpu):
@@ -872,6 +946,8 @@ def main():
                 pc[name] = measure_config(name, variant, min(args.steps, 20), args.warmup, dev,
                                           peaks, clocks, not args.no_cpu_baseline)
             pc["quantize"] = measure_quantize(dev, peaks)
+            pc["block"] = measure_block(dev, peaks)
+            torch.cuda.empty_cache()
             line["per_config"] = pc
         if not args.no_cpu_baseline:
             line["cpu_baseline"] = cpu_baseline(sh)
