@@ -8,6 +8,7 @@ CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -325,46 +326,51 @@ def mxfp4_quantize(w, codes=None, scales=None, stream=None):
 
 
 class _On:
-    """The device and stream of a call: every tensor given lies on one CUDA
-    device, which is current inside the context; outputs and scratch allocated
-    there belong to the stream the kernels run on.  (Nothing is switched for a
-    call on the current device and stream.)"""
-    __slots__ = ("device", "stream", "_ctx")
+    """A context in which the device of `t` and the stream given (that device's
+    current one if None) are current, so that outputs and scratch allocated in it
+    belong to the stream the kernels run on."""
+    __slots__ = ("_ctx",)
 
-    def __init__(self, stream, names, *tensors):
-        index = None
-        for t in tensors:
-            if t is not None:
-                i = t.get_device()
-                if i < 0 or i != index:
-                    if i < 0:
-                        bad = next(n for n, t in zip(names, tensors) if t is not None and not t.is_cuda)
-                        raise ValueError(f"{bad} must be a CUDA tensor")
-                    if index is not None:
-                        raise ValueError("tensors on different devices: " + ", ".join(
-                            f"{n} {t.device}" for n, t in zip(names, tensors) if t is not None))
-                    index = i
-                    self.device = t.device
-        here = index == torch.cuda.current_device()
-        self._ctx = None
+    def __init__(self, stream, t):
         if stream is None:
-            stream = torch.cuda.current_stream(index)
-            if not here:
-                self._ctx = torch.cuda.device(index)
+            self._ctx = torch.cuda.device(t.device)
         else:
-            if stream.device != self.device:
-                raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
+            if stream.device != t.device:
+                raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
             self._ctx = torch.cuda.stream(stream)      # also makes its device current
-        self.stream = stream.cuda_stream
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
+        self._ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        self._ctx.__exit__(*exc)
+
+
+def _elsewhere(stream, t, name):
+    """Whether a call on `t` has to switch device or stream first (see _On)."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return stream is not None or index != torch.cuda.current_device()
+
+
+def _pointers(*args):
+    """Addresses of (tensor or None, dtype, name) triples, all on the first one's
+    device, and that device's current stream.  (One pass, each check once: these
+    calls take a few microseconds on the GPU.)"""
+    index = args[0][0].get_device()
+    out = []
+    for t, dtype, name in args:
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _ptr(t, dtype, name)
+            raise ValueError("tensors on different devices: " + ", ".join(
+                f"{n} {x.device}" for x, _, n in args if x is not None))
+    out.append(torch._C._cuda_getCurrentRawStream(index))
+    return out
 
 
 def _shape(t, shape, name):
@@ -372,15 +378,18 @@ def _shape(t, shape, name):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _cache_shapes(k_cache, v_cache, kv_len, block_table, S):
+def _cache_shapes(k_cache, v_cache, kv_len, block_table, S, D):
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must be [pages, Hkv, page_size, D], block_table [S, max_pages]")
-    _shape(v_cache, k_cache.shape, "v_cache")
+    pages, Hkv, page_size, Dk = k_cache.shape
+    _shape(v_cache, (pages, Hkv, page_size, Dk), "v_cache")
     _shape(kv_len, (S,), "kv_len")
     rows, max_pages = block_table.shape
     if rows != S:
         raise ValueError(f"block_table must have {S} rows, got {rows}")
-    return (*k_cache.shape, max_pages)
+    if Dk != D:
+        raise ValueError(f"k_cache must have heads of {D}, got {Dk}")
+    return pages, Hkv, page_size, max_pages
 
 
 def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_weight=None,
@@ -391,31 +400,32 @@ def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_
     block_table [S, max_pages] int32; caches [pages, Hkv, page_size, D] bf16, updated in
     place; cos_sin [max_pos, rot] float or None (no rotation).  Returns q [S, N, Hq, D];
     rows of slots not in use are zero where the call allocates q, else left as they were."""
-    with _On(stream, ("qkv", "kv_len", "block_table", "k_cache", "v_cache", "cos_sin", "q_weight",
-                      "k_weight", "q_out"), qkv, kv_len, block_table, k_cache, v_cache, cos_sin,
-             q_weight, k_weight, q_out) as on:
-        S, N, heads, D = qkv.shape
-        pages, Hkv, page_size, Dk, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
-        if Dk != D:
-            raise ValueError(f"k_cache must have heads of {D}, got {Dk}")
-        Hq = heads - 2 * Hkv
-        if q_out is None and Hq > 0:
-            q_out = torch.zeros((S, N, Hq, D), dtype=torch.bfloat16, device=on.device)
-        _shape(q_out, (S, N, Hq, D), "q_out")
-        _shape(q_weight, (D,), "q_weight")
-        _shape(k_weight, (D,), "k_weight")
-        max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-        _check(lib().block_kv_append(
-            _ptr(qkv, torch.bfloat16, "qkv"), S, N, Hq, Hkv, D, int(norm),
-            _ptr(q_weight, torch.bfloat16, "q_weight"), _ptr(k_weight, torch.bfloat16, "k_weight"),
-            float(eps), _ptr(cos_sin, torch.float32, "cos_sin"), max_pos, rot, int(interleaved),
-            _ptr(kv_len, torch.int32, "kv_len"), _ptr(block_table, torch.int32, "block_table"),
-            max_pages, _ptr(k_cache, torch.bfloat16, "k_cache"),
-            _ptr(v_cache, torch.bfloat16, "v_cache"), pages, page_size,
-            _ptr(q_out, torch.bfloat16, "q_out"), on.stream), "block_kv_append")
+    if _elsewhere(stream, qkv, "qkv"):
+        with _On(stream, qkv):
+            return block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin, q_weight,
+                                   k_weight, norm, eps, interleaved, q_out)
+    S, N, heads, D = qkv.shape
+    pages, Hkv, page_size, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S, D)
+    Hq = heads - 2 * Hkv
+    if q_out is None and Hq > 0:
+        q_out = torch.zeros((S, N, Hq, D), dtype=torch.bfloat16, device=qkv.device)
+    _shape(q_out, (S, N, Hq, D), "q_out")
+    _shape(q_weight, (D,), "q_weight")
+    _shape(k_weight, (D,), "k_weight")
+    max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    p_qkv, p_len, p_table, p_k, p_v, p_cs, p_qw, p_kw, p_q, st = _pointers(
+        (qkv, torch.bfloat16, "qkv"), (kv_len, torch.int32, "kv_len"),
+        (block_table, torch.int32, "block_table"), (k_cache, torch.bfloat16, "k_cache"),
+        (v_cache, torch.bfloat16, "v_cache"), (cos_sin, torch.float32, "cos_sin"),
+        (q_weight, torch.bfloat16, "q_weight"), (k_weight, torch.bfloat16, "k_weight"),
+        (q_out, torch.bfloat16, "q_out"))
+    _check(lib().block_kv_append(p_qkv, S, N, Hq, Hkv, D, bool(norm), p_qw, p_kw, eps, p_cs, max_pos,
+                                 rot, bool(interleaved), p_len, p_table, max_pages, p_k, p_v, pages,
+                                 page_size, p_q, st), "block_kv_append")
     return q_out
 
 
+@functools.lru_cache(maxsize=64)
 def block_attention_workspace_bytes(S, N, Hq, Hkv, D):
     return int(lib().block_attention_workspace_bytes(S, N, Hq, Hkv, D))
 
@@ -430,24 +440,25 @@ def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window
     """Attention of N tokens per sequence over the paged cache; q [S, N, Hq, D] bf16.
 
     scale defaults to D ** -0.5; window 0 sees the whole cache.  Returns out [S, N, Hq, D]."""
-    with _On(stream, ("q", "k_cache", "v_cache", "block_table", "kv_len", "out", "workspace"),
-             q, k_cache, v_cache, block_table, kv_len, out, workspace) as on:
-        S, N, Hq, D = q.shape
-        pages, Hkv, page_size, Dk, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S)
-        if Dk != D:
-            raise ValueError(f"k_cache must have heads of {D}, got {Dk}")
-        if out is None:
-            out = torch.empty_like(q)
-        _shape(out, q.shape, "out")
-        if workspace is None:
-            workspace = alloc_attention_workspace(S, N, Hq, Hkv, D, on.device)
-        _check(lib().block_attention(
-            _ptr(q, torch.bfloat16, "q"), S, N, Hq, Hkv, D, _ptr(k_cache, torch.bfloat16, "k_cache"),
-            _ptr(v_cache, torch.bfloat16, "v_cache"), pages, page_size,
-            _ptr(block_table, torch.int32, "block_table"), max_pages,
-            _ptr(kv_len, torch.int32, "kv_len"), float(D ** -0.5 if scale is None else scale),
-            int(window), _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace"),
-            workspace.numel(), on.stream), "block_attention")
+    if _elsewhere(stream, q, "q"):
+        with _On(stream, q):
+            return block_attention(q, k_cache, v_cache, block_table, kv_len, scale, window, out,
+                                   workspace)
+    S, N, Hq, D = q.shape
+    pages, Hkv, page_size, max_pages = _cache_shapes(k_cache, v_cache, kv_len, block_table, S, D)
+    if out is None:
+        out = torch.empty_like(q)
+    _shape(out, (S, N, Hq, D), "out")
+    if workspace is None:
+        workspace = alloc_attention_workspace(S, N, Hq, Hkv, D, q.device)
+    p_q, p_k, p_v, p_table, p_len, p_out, p_ws, st = _pointers(
+        (q, torch.bfloat16, "q"), (k_cache, torch.bfloat16, "k_cache"),
+        (v_cache, torch.bfloat16, "v_cache"), (block_table, torch.int32, "block_table"),
+        (kv_len, torch.int32, "kv_len"), (out, torch.bfloat16, "out"),
+        (workspace, torch.uint8, "workspace"))
+    _check(lib().block_attention(p_q, S, N, Hq, Hkv, D, p_k, p_v, pages, page_size, p_table, max_pages,
+                                 p_len, D ** -0.5 if scale is None else scale, window, p_out, p_ws,
+                                 workspace.numel(), st), "block_attention")
     return out
 
 
@@ -457,26 +468,29 @@ def block_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p
 
     Tokens are drawn where u [S, K] is given; probabilities are written where
     with_probs is set or probs given.  The filters are [S] tensors or None (off)."""
-    with _On(stream, ("logits", "u", "temperature", "top_k", "top_p", "min_p", "token", "probs"),
-             logits, u, temperature, top_k, top_p, min_p, token, probs) as on:
-        S, K, V = logits.shape
-        _shape(u, (S, K), "u")
-        _shape(temperature, (S,), "temperature")
-        _shape(top_k, (S,), "top_k")
-        _shape(top_p, (S,), "top_p")
-        _shape(min_p, (S,), "min_p")
-        if u is not None and token is None:
-            token = torch.empty((S, K), dtype=torch.int32, device=on.device)
-        if with_probs and probs is None:
-            probs = torch.empty((S, K, V), dtype=torch.float32, device=on.device)
+    if _elsewhere(stream, logits, "logits"):
+        with _On(stream, logits):
+            return block_sample(logits, u, temperature, top_k, top_p, min_p, with_probs, token, probs)
+    S, K, V = logits.shape
+    _shape(u, (S, K), "u")
+    _shape(temperature, (S,), "temperature")
+    _shape(top_k, (S,), "top_k")
+    _shape(top_p, (S,), "top_p")
+    _shape(min_p, (S,), "min_p")
+    if token is not None:
         _shape(token, (S, K), "token")
+    elif u is not None:
+        token = torch.empty_like(u, dtype=torch.int32)
+    if probs is not None:
         _shape(probs, (S, K, V), "probs")
-        f32 = torch.float32
-        _check(lib().block_sample(
-            _ptr(logits, f32, "logits"), S, K, V, _ptr(temperature, f32, "temperature"),
-            _ptr(top_k, torch.int32, "top_k"), _ptr(top_p, f32, "top_p"), _ptr(min_p, f32, "min_p"),
-            _ptr(u, f32, "u"), _ptr(token, torch.int32, "token"), _ptr(probs, f32, "probs"),
-            on.stream), "block_sample")
+    elif with_probs:
+        probs = torch.empty_like(logits)
+    p_logits, p_t, p_k, p_p, p_m, p_u, p_token, p_probs, st = _pointers(
+        (logits, torch.float32, "logits"), (temperature, torch.float32, "temperature"),
+        (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p"),
+        (u, torch.float32, "u"), (token, torch.int32, "token"), (probs, torch.float32, "probs"))
+    _check(lib().block_sample(p_logits, S, K, V, p_t, p_k, p_p, p_m, p_u, p_token, p_probs, st),
+           "block_sample")
     return token, probs
 
 

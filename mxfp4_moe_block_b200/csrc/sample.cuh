@@ -134,6 +134,7 @@ struct SampleRow {
     u64 red[SAMPLE_WARPS];
     double redd[SAMPLE_WARPS];
     u64 wsum[SAMPLE_WARPS];
+    uint32_t warp_max[SAMPLE_WARPS];
     Found found;
     int list_n;                // tokens in this CTA's list
     int pos;
@@ -159,6 +160,12 @@ __device__ __forceinline__ void sample_copy16(void *dst, const void *src) {
                "l"(src)
                : "memory");
 }
+// A thread's arrival at the cluster's barrier that publishes nothing of its own
+// (an ordinary one first waits for the thread's own writes to be seen)
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
 // exclusive prefix of a value over the block's threads, and the block's total
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
                                                          unsigned long long *red,
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   pdl_wait();
   pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
-  cluster.barrier_arrive();       // (waited for before the first remote access)
+  cluster_arrive_relaxed();       // (waited for before the first remote access)
   const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
   const int row = blockIdx.y, s = row / a.K, V = a.V;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -210,12 +217,17 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   const int units = c1 > c0 ? (c1 - v0 + 3) / 4 : 0;
   float4 *const val4 = reinterpret_cast<float4 *>(val);
 
+  // One value of each CTA to all: warp 0 of a CTA gives it (in every lane) and
+  // publishes it; nothing else is published.
   int use = 0;                    // exchange buffer: eight uses apart, barriers between
-  auto exchange = [&](u64 v) -> const u64 * {                       // v: the same in every thread
+  auto exchange = [&](u64 v) -> const u64 * {
     u64 *mine = sh.xch[use & 7];
     ++use;
     if (tid < C) *cluster.map_shared_rank(mine + rank, tid) = v;
-    cluster.sync();
+    __syncwarp();
+    if (warp == 0) cluster.barrier_arrive();
+    else cluster_arrive_relaxed();
+    cluster.barrier_wait();
     return mine;
   };
   auto block_max = [&](u64 v) -> u64 {
@@ -228,10 +240,13 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     for (int j = 1; j < SAMPLE_WARPS; ++j) v = sh.red[j] > v ? sh.red[j] : v;
     return v;
   };
-  auto cluster_max = [&](u64 v) -> u64 {
-    const u64 *p = exchange(block_max(v));
-    u64 m = p[0];
-    for (int j = 1; j < C; ++j) m = p[j] > m ? p[j] : m;
+  auto cluster_max = [&](uint32_t v) -> uint32_t {
+    v = __reduce_max_sync(FULL, v);
+    if (lane == 0) sh.warp_max[warp] = v;
+    __syncthreads();
+    const u64 *p = exchange(warp ? 0 : __reduce_max_sync(FULL, sh.warp_max[lane % SAMPLE_WARPS]));
+    uint32_t m = (uint32_t)p[0];
+    for (int j = 1; j < C; ++j) m = max(m, (uint32_t)p[j]);
     return m;
   };
 
@@ -260,7 +275,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     most = fmaxf(most, fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));    // (skips NaN)
   }
   cluster.barrier_wait();
-  uint32_t top_key = (uint32_t)cluster_max(logit_key(most));
+  const uint32_t top_key = cluster_max(logit_key(most));
   float top = key_logit(top_key);
   // +infinity takes all mass: such a row counts as 0 there and -infinity elsewhere
   const bool inf_row = top == INFINITY;
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           break;
         }
       }
-      first = (uint32_t)cluster_max(first);
+      first = cluster_max(first);
     }
     const int top_token = (int)~first;
     if (rank == 0 && tid == 0) {
@@ -751,15 +766,15 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         above = f.above;
         mass_above = f.mass_above;
         if (bits < 0) {
-          u64 hi = 0, lo = 0;
+          uint32_t hi = 0, lo = 0;
           for_kept([&](float l) {
             if ((by_mass && !z.positive(l)) || bucket_of(l) != f.bucket) return;
             const uint32_t key = logit_key(l);
             hi = key > hi ? key : hi;
-            lo = (uint32_t)~key > lo ? (uint32_t)~key : lo;
+            lo = ~key > lo ? ~key : lo;
           });
-          khi = (uint32_t)cluster_max(hi);
-          klo = ~(uint32_t)cluster_max(lo);
+          khi = cluster_max(hi);
+          klo = ~cluster_max(lo);
         } else {
           khi -= (uint32_t)f.bucket << bits;
           const uint32_t width = (1u << bits) - 1;
@@ -877,14 +892,14 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     sh.redd[warp] = wsum;
   }
   __syncthreads();
-  u64 cta_mass = 0;
-  double cta_w = 0.0;
+  u64 cta_mass = 0;                // (of warp 0, which adds the warps' up)
+  if (warp == 0) {
+    cta_mass = warp_sum_u64(lane < SAMPLE_WARPS ? sh.wsum[lane] : 0);
+    double cta_w = lane < SAMPLE_WARPS ? sh.redd[lane] : 0.0;
 #pragma unroll
-  for (int j = 0; j < SAMPLE_WARPS; ++j) {
-    cta_mass += sh.wsum[j];
-    cta_w += sh.redd[j];
+    for (int o = 16; o > 0; o >>= 1) cta_w += __shfl_xor_sync(FULL, cta_w, o);
+    if (lane < C) *cluster.map_shared_rank(&sh.xchd[rank], lane) = cta_w;
   }
-  if (tid < C) *cluster.map_shared_rank(&sh.xchd[rank], tid) = cta_w;
   const u64 *pm = exchange(cta_mass);
   u64 total = 0, before = 0;
   double sum = 0.0;
@@ -893,6 +908,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     total += pm[j];
     sum += sh.xchd[j];
   }
+  cta_mass = pm[rank];
   // (no CTA leaves before every other has finished writing to it: the exchange
   // above was the last remote access)
 
