@@ -120,9 +120,8 @@ __device__ __forceinline__ unsigned long long sample_mass(double w40) {
 struct SampleRow {
   typedef unsigned long long u64;
   struct Found {               // what the first CTA tells the others
-    int bucket, count;         // bucket of the threshold, its tokens
-    u64 above, mass_above;     // tokens and mass of the buckets before it
-    u64 upto;                  // tokens up to and with it
+    int bucket, count;         // bucket of the threshold, its tokens (by count)
+    u64 above, mass_above;     // tokens or mass of the buckets before it
     u64 bar;                   // top-p's mass
     uint32_t thr;
     int cut;
@@ -137,6 +136,7 @@ struct SampleRow {
     uint32_t warp_max[SAMPLE_WARPS];
     Found found;
     int list_n;                // tokens in this CTA's list
+    int above_n;               // and of its slice above the threshold's bucket
     int pos;
   };
 };
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // full warps: few are kept as a rule, and they wait in the warp's queue (in the
   // list's place) until there is one for every lane.  `zero`: the others become 0.
   const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
-  bool many = false;                             // top-p keeps a sixth of the row or more
+  bool many = false;                             // top-p keeps a sixth of the slice or more
   float least = z.below;                         // x - top below which no token is kept
   auto for_queued = [&](auto f, bool zero = false) {
     uint32_t *const queue = reinterpret_cast<uint32_t *>(list) + warp * SAMPLE_QUEUE;
@@ -413,35 +413,38 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     auto find = [&](bool by_mass, u64 want, u64 above, u64 mass_above, u64 bar) -> SampleRow::Found {
       cluster.sync();
       if (rank == 0) {
-        u64 n[2] = {0, 0}, m[2] = {0, 0};
+        u64 n[2] = {0, 0};                       // tokens or mass of this thread's two buckets
 #pragma unroll
         for (int r = 0; r < SAMPLE_MAX_CLUSTER; ++r) {
           if (r >= C) break;
           const uint32_t *rc = cluster.map_shared_rank(h_cnt, r);
-          const uint2 cnt = *reinterpret_cast<const uint2 *>(rc + 2 * tid);
-          n[0] += cnt.x;
-          n[1] += cnt.y;
           if (by_mass) {
             const uint2 lo = *reinterpret_cast<const uint2 *>(rc + SAMPLE_BUCKETS + 2 * tid);
             const uint2 hi = *reinterpret_cast<const uint2 *>(rc + 2 * SAMPLE_BUCKETS + 2 * tid);
-            m[0] += ((u64)hi.x << 32) + lo.x;
-            m[1] += ((u64)hi.y << 32) + lo.y;
+            n[0] += ((u64)hi.x << 32) + lo.x;
+            n[1] += ((u64)hi.y << 32) + lo.y;
+          } else {
+            const uint2 cnt = *reinterpret_cast<const uint2 *>(rc + 2 * tid);
+            n[0] += cnt.x;
+            n[1] += cnt.y;
           }
         }
-        u64 tn, tm = 0, bm = 0;
-        const u64 bn = block_scan(n[0] + n[1], sh.red, tn);
-        if (by_mass) bm = block_scan(m[0] + m[1], sh.red, tm);
-        if (by_mass && bar == 0) {
-          bar = p > 0.0 ? (u64)ceil(p * (double)tm) : 1;
-          if (bar < 1) bar = 1;
+        u64 all;
+        u64 run = (by_mass ? mass_above : above) + block_scan(n[0] + n[1], sh.red, all);
+        if (by_mass) {
+          if (bar == 0) {
+            bar = p > 0.0 ? (u64)ceil(p * (double)all) : 1;
+            if (bar < 1) bar = 1;
+          }
+          want = bar;
+        } else if (tid == 0 && above + all < want) {
+          sh.found.bucket = -1;
         }
-        if (!by_mass && tid == 0 && above + tn < want) sh.found.bucket = -1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const u64 pn = above + bn + (i ? n[0] : 0), pm = mass_above + bm + (i ? m[0] : 0);
-          const bool here = by_mass ? pm < bar && bar <= pm + m[i] : pn < want && want <= pn + n[i];
-          if (here)
-            sh.found = SampleRow::Found{2 * tid + i, (int)n[i], pn, pm, pn + n[i], bar, 0, 0, 0.f};
+          if (run < want && want <= run + n[i])
+            sh.found = SampleRow::Found{2 * tid + i, (int)n[i], run, run, bar, 0, 0, 0.f};
+          run += n[i];
         }
       }
       cluster.sync();
@@ -697,12 +700,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           return key < klo || key > khi ? -1 : (int)((khi - key) >> bits);
         };
         clear();
-        if (tid == 0) sh.list_n = 0;
+        if (tid == 0) sh.list_n = sh.above_n = 0;
         if (by_mass) {                           // (tokens without weight are not in question)
           auto add = [&](float l, u64 m) {
             const int b = z.positive(l) ? bucket_of(l) : -1;
             if (b < 0) return;
-            atomicAdd(h_cnt + b, 1u);
             const uint32_t lo = (uint32_t)m, old = atomicAdd(h_lo + b, lo);
             const uint32_t hi = (uint32_t)(m >> 32) + (old + lo < old ? 1u : 0u);
             if (hi) atomicAdd(h_hi + b, hi);
@@ -729,41 +731,53 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         f = find(by_mass, want, above, mass_above, bar);
         if (f.bucket < 0) return;                // fewer tokens than wanted (the rest is NaN)
         bar = f.bar;
-        if (by_mass) many = f.upto * 6 > (u64)V;
-        if (f.count <= SAMPLE_LIST) {
-          cluster.sync();                        // (found is read; it takes the answer)
+        if (by_mass || f.count <= SAMPLE_LIST) {
           // (tested without the conversions and the logit's key)
+          int higher = 0;                        // kept tokens above the bucket
           if (bits < 0) {
             const float from = (float)f.bucket;
             const float to = f.bucket == SAMPLE_BUCKETS - 1 ? NAN : (float)(f.bucket + 1);
             collect([&](float l) {
               const float d = (top - l) * scale;
+              higher += d < from;
               return d >= from && !(d >= to) && (!by_mass || z.positive(l));
             });
           } else {
             const uint32_t up = khi - ((uint32_t)f.bucket << bits), width = (1u << bits) - 1;
             const float from = key_logit(up), to = key_logit(up - klo > width ? up - width : klo);
-            collect([&](float l) { return l <= from && l >= to && (!by_mass || z.positive(l)); });
+            collect([&](float l) {
+              higher += l > from;
+              return l <= from && l >= to && (!by_mass || z.positive(l));
+            });
+          }
+          if (by_mass) {
+            higher = __reduce_add_sync(FULL, higher);
+            if (lane == 0) atomicAdd(&sh.above_n, higher);
           }
           cluster.sync();
-          if (rank == 0) {
-            u64 v[PER], m[PER];
-            take_lists(min(list_total(), SAMPLE_LIST), v);
+          const int n = by_mass ? list_total() : f.count;
+          if (n <= SAMPLE_LIST) {
+            if (by_mass) many = (sh.above_n + n) * 6 > units * 4;
+            if (rank == 0) {
+              u64 v[PER], m[PER];
+              take_lists(n, v);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) m[j] = by_mass && v[j] ? mass_at(word_logit(v[j])) : 0;
-            const u64 last = pick(v, m, by_mass, by_mass ? bar - f.mass_above : want - f.above);
-            if (tid == 0) {
-              sh.found.thr = (uint32_t)(last >> 32);
-              sh.found.cut = (int)~(uint32_t)last;
+              for (int j = 0; j < PER; ++j) m[j] = by_mass && v[j] ? mass_at(word_logit(v[j])) : 0;
+              const u64 last = pick(v, m, by_mass, by_mass ? bar - f.mass_above : want - f.above);
+              if (tid == 0) {
+                sh.found.thr = (uint32_t)(last >> 32);
+                sh.found.cut = (int)~(uint32_t)last;
+              }
             }
+            cluster.sync();
+            cut_to(lead->thr, lead->cut);        // (found is not written before the next barrier)
+            return;
           }
-          cluster.sync();
-          cut_to(lead->thr, lead->cut);
-          cluster.sync();                        // (found is free for the next filter)
-          return;
+          many = true;                           // thousands of nearly equal logits at the border
+          cluster.sync();                        // (the lists' lengths are read)
         }
         // more tokens than the list holds: the keys of this bucket
-        above = f.above;
+        above = f.above;                         // (the one of the two that counts)
         mass_above = f.mass_above;
         if (bits < 0) {
           uint32_t hi = 0, lo = 0;
