@@ -84,11 +84,16 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // at Chebyshev nodes: 2^-40, the masses' own step.  11 double operations and
 // two conversions.
 struct SampleScale {
-  double top, c;
-  float ftop, fc, below;          // weights of x - top <= below are 0
-  __device__ __forceinline__ SampleScale(float t, double scale)
-      : top((double)t), c(scale), ftop(t), fc((float)c), below((float)(-1000.0 / c)) {}
-  __device__ __forceinline__ bool positive(float x) const { return x - ftop > below; }   // NaN: no
+  double top, c, halving;         // halving: logits to a factor of two
+  float ftop, fc, lowest;         // logits below `lowest` (d c < -1000) weigh 0
+  __device__ __forceinline__ SampleScale(float t, double temperature)
+      : top((double)t), c(1.4426950408889634 / temperature),
+        halving(temperature * 0.6931471805599453), ftop(t), fc((float)c) {
+    const double least = fma(-1000.0, halving, top);
+    lowest = fmaxf((float)least, -FLT_MAX);
+    if ((double)lowest < least) lowest = key_logit(logit_key(lowest) + 1);   // (rounded down)
+  }
+  __device__ __forceinline__ bool positive(float x) const { return x >= lowest; }   // NaN: no
   __device__ __forceinline__ double weight(float x) const {
     const float magic = 12582912.f + 40.f;                          // 1.5 2^23, and the 2^40
     const float shifted = fmaf(x - ftop, fc, magic);
@@ -133,7 +138,7 @@ struct SampleRow {
     u64 red[SAMPLE_WARPS];
     double redd[SAMPLE_WARPS];
     u64 wsum[SAMPLE_WARPS];
-    uint32_t warp_max[SAMPLE_WARPS];
+    alignas(16) uint32_t warp_max[2 * SAMPLE_WARPS];
     Found found;
     int list_n;                // tokens in this CTA's list
     int above_n;               // and of its slice above the threshold's bucket
@@ -144,14 +149,6 @@ struct SampleRow {
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-  return v;
-}
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long w = __shfl_xor_sync(FULL, v, o);
-    v = w > v ? w : v;
-  }
   return v;
 }
 __device__ __forceinline__ void sample_copy16(void *dst, const void *src) {
@@ -229,16 +226,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     else cluster_arrive_relaxed();
     cluster.barrier_wait();
     return mine;
-  };
-  auto block_max = [&](u64 v) -> u64 {
-    v = warp_max_u64(v);
-    __syncthreads();
-    if (lane == 0) sh.red[warp] = v;
-    __syncthreads();
-    v = sh.red[0];
-#pragma unroll
-    for (int j = 1; j < SAMPLE_WARPS; ++j) v = sh.red[j] > v ? sh.red[j] : v;
-    return v;
   };
   auto cluster_max = [&](uint32_t v) -> uint32_t {
     v = __reduce_max_sync(FULL, v);
@@ -333,7 +320,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     return;                                       // (no remote access after the exchange)
   }
   // (limits that keep the scale, its reciprocal and its products finite in float)
-  const SampleScale z(top, 1.4426950408889634 / fmin(fmax(T, 1e-36), 1e30));
+  const SampleScale z(top, fmin(fmax(T, 1e-36), 1e30));
   auto mass_at = [&](float l) -> u64 { return z.positive(l) ? sample_mass(z.weight(l)) : 0; };
 
   // ---- the threshold: kept are logits above `at`, and at it the tokens <= last ----
@@ -354,10 +341,12 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // list's place) until there is one for every lane.  `zero`: the others become 0.
   const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
   bool many = false;                             // top-p keeps a sixth of the slice or more
-  float least = z.below;                         // x - top below which no token is kept
+  float least = -INFINITY;                       // no token below this logit is kept
   auto for_queued = [&](auto f, bool zero = false) {
     uint32_t *const queue = reinterpret_cast<uint32_t *>(list) + warp * SAMPLE_QUEUE;
     const int j1 = min(units, (warp + 1) * wu);
+    const float from = fmaxf(fmaxf(at, z.lowest), least);
+    const int upto = from == at ? last : 0x7fffffff;                // of the tokens at `from`
     int waiting = 0;
     auto serve = [&](int n) {                                       // the queue's last n
       waiting -= n;
@@ -371,7 +360,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       bool keep[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        keep[i] = z.positive(e[i]) && e[i] - z.ftop >= least && kept(e[i], v0 + 4 * j + i);
+        keep[i] = e[i] > from || (e[i] == from && v0 + 4 * j + i <= upto);
       if (__any_sync(FULL, keep[0] || keep[1] || keep[2] || keep[3])) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -458,11 +447,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         const float e[4] = {q.x, q.y, q.z, q.w};
         bool take[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) take[i] = test(e[i]) && kept(e[i], v0 + 4 * j + i);
+        for (int i = 0; i < 4; ++i) take[i] = test(e[i]);
         if (!(take[0] || take[1] || take[2] || take[3])) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (take[i]) {
+          if (take[i] && kept(e[i], v0 + 4 * j + i)) {
             const int to = atomicAdd(&sh.list_n, 1);
             if (to < SAMPLE_LIST)
               list[to] = ((u64)logit_key(e[i]) << 32) | (uint32_t)~(uint32_t)(v0 + 4 * j + i);
@@ -495,26 +484,51 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     auto word_logit = [&](u64 v) { return key_logit((uint32_t)(v >> 32)); };
     // The word down to which the words (0: none) reach `want` in count or mass.  A
     // histogram over the range of those in question, as often as more than a
-    // warp's worth is left.
+    // warp's worth is left: of their keys, then, where those are equal, of ~index.
     auto pick = [&](const u64 (&v)[PER], const u64 (&m)[PER], bool by_mass, u64 want) -> u64 {
-      u64 floor = 1, ceiling = ~0ull, above = 0;             // words in question, sum of those before
+      uint32_t klo = 1, khi = 0xffffffffu, tlo = 0, thi = 0xffffffffu;   // in question
+      u64 above = 0;                                         // sum of those before
+      auto key_of = [](u64 w) { return (uint32_t)(w >> 32); };
+      auto asked = [&](u64 w) {
+        return key_of(w) >= klo && key_of(w) <= khi && (uint32_t)w >= tlo && (uint32_t)w <= thi;
+      };
       for (;;) {
-        u64 hi = 0, lo = 0;
+        const bool by_key = klo != khi;
+        uint32_t hi = 0, lo = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (v[j] >= floor && v[j] <= ceiling) {
-            hi = v[j] > hi ? v[j] : hi;
-            lo = ~v[j] > lo ? ~v[j] : lo;
+          if (asked(v[j])) {
+            const uint32_t x = by_key ? key_of(v[j]) : (uint32_t)v[j];
+            hi = max(hi, x);
+            lo = max(lo, ~x);
           }
-        hi = block_max(hi);
-        lo = ~block_max(lo);
-        if (hi <= lo) return hi;
-        const int width = 64 - __clzll((long long)(hi - lo)), shift = width > 10 ? width - 10 : 0;
-        clear();
+        hi = __reduce_max_sync(FULL, hi);
+        lo = __reduce_max_sync(FULL, lo);
+        __syncthreads();
+        if (lane == 0) {
+          sh.warp_max[warp] = hi;
+          sh.warp_max[SAMPLE_WARPS + warp] = lo;
+        }
+        for (int i = tid; i < SAMPLE_BUCKETS; i += SAMPLE_THREADS) h_cnt[i] = h_lo[i] = h_hi[i] = 0;
+        __syncthreads();
+        const uint4 *const most4 = reinterpret_cast<const uint4 *>(sh.warp_max);
+#pragma unroll
+        for (int j = 0; j < SAMPLE_WARPS / 4; ++j) {
+          const uint4 a = most4[j], b = most4[SAMPLE_WARPS / 4 + j];
+          hi = max(max(hi, max(a.x, a.y)), max(a.z, a.w));
+          lo = max(max(lo, max(b.x, b.y)), max(b.z, b.w));
+        }
+        lo = ~lo;
+        if (hi == lo) {                                      // one key: by index; one word: found
+          if (!by_key) return ((u64)khi << 32) | hi;
+          klo = khi = hi;
+          continue;
+        }
+        const int width = 32 - __clz(hi - lo), shift = width > 10 ? width - 10 : 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (v[j] >= lo && v[j] <= hi) {
-            const int b = (int)((hi - v[j]) >> shift);
+          if (asked(v[j])) {
+            const int b = (int)((hi - (by_key ? key_of(v[j]) : (uint32_t)v[j])) >> shift);
             atomicAdd(h_cnt + b, 1u);
             if (by_mass) {
               const uint32_t x = (uint32_t)m[j], old = atomicAdd(h_lo + b, x);
@@ -540,8 +554,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         if (tid == 0) sh.pos = 0;
         __syncthreads();
         above = sh.found.above;
-        ceiling = hi - ((u64)sh.found.bucket << shift);
-        floor = ceiling - lo >= (1ull << shift) ? ceiling - ((1ull << shift) - 1) : lo;
+        const uint32_t up = hi - ((uint32_t)sh.found.bucket << shift), step = (1u << shift) - 1;
+        const uint32_t down = up - lo > step ? up - step : lo;
+        if (by_key) klo = down, khi = up;
+        else tlo = down, thi = up;
         const int count = sh.found.count;
         if (count > 32) continue;
         // the last few: ranks by comparing in one warp
@@ -549,7 +565,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         __syncthreads();                         // (the histogram is read)
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-          if (v[j] >= floor && v[j] <= ceiling) {
+          if (asked(v[j])) {
             const int at = atomicAdd(&sh.pos, 1);
             few[2 * at] = v[j];
             few[2 * at + 1] = by_mass ? m[j] : 1;
@@ -878,8 +894,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     const std::true_type yes;
     const std::false_type no;
     if ((cutting || low) && !many) {
-      // min-p in advance, with room for what float loses; exact by the mass
-      least = low ? (float)((log2((double)low) - 40.0) / z.c) * 1.0001f - 1e-30f : z.below;
+      // min-p in advance, with room for what float loses (4e-6); exact by the mass
+      if (low) least = (float)fma((double)(log2f((float)low) - 40.f - 1e-4f), z.halving, z.top);
       for_queued([&](uint32_t i) {
         const double w = z.weight(val[i]);
         const u64 m = sample_mass(w);
