@@ -14,7 +14,7 @@
 // A thread-block cluster per row: each CTA brings its slice of the row into
 // shared memory once and every later pass reads it there.  The threshold is
 // found without sorting the row: a histogram of the distance to the maximum
-// (counts, and exact masses where top-p needs them) over 1024 buckets names the
+// (counts, or the exact masses where top-p needs them) over 1024 buckets names the
 // bucket of the threshold, whose few tokens go to the cluster's first CTA; with
 // four words (logit, ~index) to a thread it narrows them by histograms of its own
 // and ranks the last 32 by comparing.  A bucket with more tokens than that list
@@ -29,13 +29,14 @@
 // takes 12 (and two conversions, 16 a cycle), ~5 weights per cycle and SM, against
 // ~6 logits per cycle that HBM delivers to an SM.  So a kept token's weight is
 // computed once (top-p over a whole row: every weight, and the kept ones again);
-// where few are kept (top-k, top-p) they wait in a queue until a warp has 32 of
-// them; the float of a weight stays in shared memory for the probabilities.  And
-// the row's steps one after another: five to nine barriers of the cluster and the
-// first CTA's search between them, ~11 us for a row of 32000, hidden by other rows
-// only as far as two CTAs fit an SM.  Measured: one row of 32000 (top-k 50, top-p
-// and min-p) 14 us; 128 rows of 152064 with mixed filters, tokens only, 139 us
-// (24 us at HBM's rate); 1024 rows of 32000 with probabilities 109 us (40 us).
+// where few are kept they wait in a queue until a warp has 32 of them; the float of
+// a weight stays in shared memory for the probabilities.  And the row's steps one
+// after another: five to nine barriers of the cluster and the first CTA's search
+// between them, 8 us for a row of 32000 without filters, 19 with top-p, hidden by
+// other rows only as far as two CTAs fit an SM (issue slots 58 % busy, DRAM 16 %).
+// Measured, with probabilities: 128 rows of 152064, mixed filters, 122 us (24 us at
+// HBM's rate); 1024 rows of 32000, temperature 107 us (40 us), top-k 50 135 us,
+// top-p 0.9 266 us; one row of 32000 under every filter, token only, 13 us.
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -340,7 +341,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // full warps: few are kept as a rule, and they wait in the warp's queue (in the
   // list's place) until there is one for every lane.  `zero`: the others become 0.
   const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
-  bool many = false;                             // top-p keeps a sixth of the slice or more
+  // top-p keeps a third of the slice or more: then each weight where it stands, else
+  // the queue (1024 rows of 32000, top-p 0.9: queue 266 us, in place 274; 0.99: 289
+  // and 276; top-p 0.7 252 and 269)
+  bool many = false;
   float least = -INFINITY;                       // no token below this logit is kept
   auto for_queued = [&](auto f, bool zero = false) {
     uint32_t *const queue = reinterpret_cast<uint32_t *>(list) + warp * SAMPLE_QUEUE;
@@ -590,7 +594,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
       return (int)fminf((top - l) * scale, (float)(SAMPLE_BUCKETS - 1));
     };
 
-    // ---- a small top-k: the first CTA settles the row ----
+    // ---- a small top-k: the first CTA settles the row (1024 rows of 32000, top-k 50:
+    // 135 us, by the histograms below 173; with top-p 0.9 beside it 144 and 257) ----
     // Every CTA lists its tokens down to the k-th largest of its threads' own maxima:
     // the k first-ranked of the row are among them, and few more than k of each CTA.
     SampleRow::Found f{};
@@ -773,7 +778,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
           cluster.sync();
           const int n = by_mass ? list_total() : f.count;
           if (n <= SAMPLE_LIST) {
-            if (by_mass) many = (sh.above_n + n) * 6 > units * 4;
+            if (by_mass) many = (sh.above_n + n) * 3 > units * 4;
             if (rank == 0) {
               u64 v[PER], m[PER];
               take_lists(n, v);
