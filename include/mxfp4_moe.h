@@ -430,7 +430,7 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
  *   pages that no token of the block sees, are never used, whatever they or
  *   their page ids hold; a key or value that is not finite reaches the tokens
  *   that see it and no others.
- *   q, out      [S, N, Hq, D] bf16
+ *   q, out      [S, N, Hq, D] bf16; out must not overlap the inputs
  *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16
  *   block_table [S, max_pages] int32; kv_len [S] int32
  *   workspace   device scratch of block_attention_workspace_bytes bytes,

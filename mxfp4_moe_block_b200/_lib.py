@@ -419,8 +419,8 @@ def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_
         (v_cache, torch.bfloat16, "v_cache"), (cos_sin, torch.float32, "cos_sin"),
         (q_weight, torch.bfloat16, "q_weight"), (k_weight, torch.bfloat16, "k_weight"),
         (q_out, torch.bfloat16, "q_out"))
-    _check(lib().block_kv_append(p_qkv, S, N, Hq, Hkv, D, bool(norm), p_qw, p_kw, eps, p_cs, max_pos,
-                                 rot, bool(interleaved), p_len, p_table, max_pages, p_k, p_v, pages,
+    _check(lib().block_kv_append(p_qkv, S, N, Hq, Hkv, D, int(norm), p_qw, p_kw, float(eps), p_cs, max_pos,
+                                 rot, int(interleaved), p_len, p_table, max_pages, p_k, p_v, pages,
                                  page_size, p_q, st), "block_kv_append")
     return q_out
 
@@ -456,9 +456,10 @@ def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window
         (v_cache, torch.bfloat16, "v_cache"), (block_table, torch.int32, "block_table"),
         (kv_len, torch.int32, "kv_len"), (out, torch.bfloat16, "out"),
         (workspace, torch.uint8, "workspace"))
-    _check(lib().block_attention(p_q, S, N, Hq, Hkv, D, p_k, p_v, pages, page_size, p_table, max_pages,
-                                 p_len, D ** -0.5 if scale is None else scale, window, p_out, p_ws,
-                                 workspace.numel(), st), "block_attention")
+    _check(lib().block_attention(
+        p_q, S, N, Hq, Hkv, D, p_k, p_v, pages, page_size, p_table, max_pages, p_len,
+        D ** -0.5 if scale is None else float(scale), int(window), p_out, p_ws, workspace.numel(), st),
+        "block_attention")
     return out
 
 
@@ -506,5 +507,5 @@ def moe_clear_device_status(stream=None):
 
 
 def moe_set_wait_limit_ns(ns=0, stream=None):
-    """Limit of the FFN kernels' bounded waits (0 = the 2 s default)."""
+    """Limit of the FFN and attention kernels' bounded waits (0 = the 2 s default)."""
     _check(lib().moe_set_wait_limit_ns(int(ns), _stream(stream)), "moe_set_wait_limit_ns")
