@@ -351,26 +351,41 @@ def _elsewhere(stream, t, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != torch._C._cuda_getDevice()
 
 
-def _pointers(*args):
-    """Addresses of (tensor or None, dtype, name) triples, all on the first one's
-    device, and that device's current stream.  (One pass, each check once: these
-    calls take a few microseconds on the GPU.)"""
-    index = args[0][0].get_device()
+_device_of, _is_contiguous, _address = (torch.Tensor.get_device, torch.Tensor.is_contiguous,
+                                        torch.Tensor.data_ptr)
+
+
+def _pointers(kinds, *tensors):
+    """Addresses of tensors (or None) of the given (name, dtype) kinds, all on the
+    first one's device, and that device's current stream.  (One pass, each check once:
+    these calls take a few microseconds on the GPU.)"""
+    index = _device_of(tensors[0])
     out = []
-    for t, dtype, name in args:
+    for t, (name, dtype) in zip(tensors, kinds):
         if t is None:
             out.append(None)
-        elif t.dtype is dtype and t.get_device() == index and t.is_contiguous():
-            out.append(t.data_ptr())
+        elif t.dtype is dtype and _device_of(t) == index and _is_contiguous(t):
+            out.append(_address(t))
         else:
             _ptr(t, dtype, name)
             raise ValueError("tensors on different devices: " + ", ".join(
-                f"{n} {x.device}" for x, _, n in args if x is not None))
+                f"{n} {x.device}" for x, (n, _) in zip(tensors, kinds) if x is not None))
     out.append(torch._C._cuda_getCurrentRawStream(index))
     return out
+
+
+_APPEND = (("qkv", torch.bfloat16), ("kv_len", torch.int32), ("block_table", torch.int32),
+           ("k_cache", torch.bfloat16), ("v_cache", torch.bfloat16), ("cos_sin", torch.float32),
+           ("q_weight", torch.bfloat16), ("k_weight", torch.bfloat16), ("q_out", torch.bfloat16))
+_ATTENTION = (("q", torch.bfloat16), ("k_cache", torch.bfloat16), ("v_cache", torch.bfloat16),
+              ("block_table", torch.int32), ("kv_len", torch.int32), ("out", torch.bfloat16),
+              ("workspace", torch.uint8))
+_SAMPLE = (("logits", torch.float32), ("temperature", torch.float32), ("top_k", torch.int32),
+           ("top_p", torch.float32), ("min_p", torch.float32), ("u", torch.float32),
+           ("token", torch.int32), ("probs", torch.float32))
 
 
 def _shape(t, shape, name):
@@ -414,11 +429,7 @@ def block_kv_append(qkv, kv_len, block_table, k_cache, v_cache, cos_sin=None, q_
     _shape(k_weight, (D,), "k_weight")
     max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
     p_qkv, p_len, p_table, p_k, p_v, p_cs, p_qw, p_kw, p_q, st = _pointers(
-        (qkv, torch.bfloat16, "qkv"), (kv_len, torch.int32, "kv_len"),
-        (block_table, torch.int32, "block_table"), (k_cache, torch.bfloat16, "k_cache"),
-        (v_cache, torch.bfloat16, "v_cache"), (cos_sin, torch.float32, "cos_sin"),
-        (q_weight, torch.bfloat16, "q_weight"), (k_weight, torch.bfloat16, "k_weight"),
-        (q_out, torch.bfloat16, "q_out"))
+        _APPEND, qkv, kv_len, block_table, k_cache, v_cache, cos_sin, q_weight, k_weight, q_out)
     _check(lib().block_kv_append(p_qkv, S, N, Hq, Hkv, D, int(norm), p_qw, p_kw, float(eps), p_cs, max_pos,
                                  rot, int(interleaved), p_len, p_table, max_pages, p_k, p_v, pages,
                                  page_size, p_q, st), "block_kv_append")
@@ -452,10 +463,7 @@ def block_attention(q, k_cache, v_cache, block_table, kv_len, scale=None, window
     if workspace is None:
         workspace = alloc_attention_workspace(S, N, Hq, Hkv, D, q.device)
     p_q, p_k, p_v, p_table, p_len, p_out, p_ws, st = _pointers(
-        (q, torch.bfloat16, "q"), (k_cache, torch.bfloat16, "k_cache"),
-        (v_cache, torch.bfloat16, "v_cache"), (block_table, torch.int32, "block_table"),
-        (kv_len, torch.int32, "kv_len"), (out, torch.bfloat16, "out"),
-        (workspace, torch.uint8, "workspace"))
+        _ATTENTION, q, k_cache, v_cache, block_table, kv_len, out, workspace)
     _check(lib().block_attention(
         p_q, S, N, Hq, Hkv, D, p_k, p_v, pages, page_size, p_table, max_pages, p_len,
         D ** -0.5 if scale is None else float(scale), int(window), p_out, p_ws, workspace.numel(), st),
@@ -487,9 +495,7 @@ def block_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p
     elif with_probs:
         probs = torch.empty_like(logits)
     p_logits, p_t, p_k, p_p, p_m, p_u, p_token, p_probs, st = _pointers(
-        (logits, torch.float32, "logits"), (temperature, torch.float32, "temperature"),
-        (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p"),
-        (u, torch.float32, "u"), (token, torch.int32, "token"), (probs, torch.float32, "probs"))
+        _SAMPLE, logits, temperature, top_k, top_p, min_p, u, token, probs)
     _check(lib().block_sample(p_logits, S, K, V, p_t, p_k, p_p, p_m, p_u, p_token, p_probs, st),
            "block_sample")
     return token, probs
