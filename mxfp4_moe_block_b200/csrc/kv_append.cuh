@@ -15,16 +15,17 @@
 // lane; the rotation's partner of a lane is a fixed lane of the group (rot is
 // a multiple of 16, so rot/2 is a whole number of lanes), reached by a
 // shuffle.  The heads are asked for before the token's place is looked up, and
-// four CTAs of 64 registers share an SM (43 us below with three).  Measured: one
-// token of 80 heads 2.5 us, 128 tokens of 56 heads 3.3 us (the launch), 4224
-// tokens of 80 heads of 128 39 us: 175 MB at 4.5 TB/s, 0.69 of a plain copy's rate
-// (the norms' shuffles and the rotation fill the issue slots beside the loads).
+// eight CTAs of 128 threads and 64 registers share an SM (the largest case below:
+// 37.4 us, with four of 256 threads 39.0, with three 43).  Measured: one token of 80
+// heads 2.4 us, 128 tokens of 56 heads 3.4 us (the launch), 4224 tokens of 80 heads
+// of 128 37 us: 175 MB at 4.7 TB/s, 0.72 of a plain copy's rate (the norms' shuffles
+// and the rotation fill the issue slots beside the loads).
 #pragma once
 #include "common.cuh"
 
 namespace moe {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_THREADS = 128;
 
 struct AppendArgs {
   const uint16_t *qkv;           // [S*N, Hq + 2*Hkv, D]
@@ -53,10 +54,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// grid (S*N tokens, groups of HPT * 256/(D/8) heads).  Each lane group takes
+// grid (S*N tokens, groups of HPT * 128/(D/8) heads).  Each lane group takes
 // HPT heads of its token, so that the cosines and sines are read once for all.
 template <int D, int HPT>
-__global__ void __launch_bounds__(APPEND_THREADS, 4)
+__global__ void __launch_bounds__(APPEND_THREADS, 8)
 kv_append_kernel(const AppendArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -177,10 +178,10 @@ kv_append_kernel(const AppendArgs a) {
   }
 }
 
-// Heads per lane group: one where the tokens are few (one token of 80 heads: 2.5
+// Heads per lane group: one where the tokens are few (one token of 80 heads: 2.4
 // us with one, 4.1 with five), up to five, in equal shares, where each SM has four
-// CTAs of tokens all the same (4224 tokens x 80 heads of 128: 69 us with one, 39
-// with five).
+// CTAs of tokens all the same (4224 tokens x 80 heads of 128: 69 us with one, 46
+// with up to three, 37 with five).
 template <int HPT>
 inline cudaError_t launch_append_hpt(const AppendArgs &a, int T, int D, cudaStream_t s) {
   const int heads = a.Hq + 2 * a.Hkv;
