@@ -883,7 +883,15 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tc_wait_st();
           } else {
+            // A warp without rows must not run a phase ahead of the others either: S(t + 2)
+            // may come as soon as S(t) is read, and a second arrival of this warp would
+            // then complete P(t) in the place of a warp that still writes it.
             mbar_arrive(s_free + (t & 1));
+            if (t >= 2) {
+              ok = attn_wait(pv_done + (t & 1), ((t - 2) >> 1) & 1, abort_flag);
+              ok = __all_sync(FULL, ok);
+              if (!ok) break;
+            }
           }
           tc_fence_before();
           mbar_arrive(p_full + (t & 1));

@@ -1,0 +1,85 @@
+"""GPU checks of the block's append, attention and sampling where several of
+their parts meet: rows that fill a block in part over many tiles, values that
+are not finite, masses at a filter's border.
+
+The attention is compared with `attention64`, the definition in float64 on the
+device (the oracle's loops are too slow for these sizes), under the tolerance
+that test_gpu_block.py derives.
+"""
+import pytest
+import torch
+
+import mxfp4_moe_block_b200 as mm
+from test_gpu_block import DEV, EPS, HALF, attention_case, clean_status, to_dev  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attention64(d, window, scale=None):
+    """(out, spread) in float64: softmax of the keys a token sees, and the weighted
+    mean of |v|, which rounding errors of the weights scale with."""
+    S, N, Hq, D = d["q"].shape
+    pages, Hkv, page, _ = d["k_cache"].shape
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.zeros((S, N, Hq, D), dtype=torch.float64, device=DEV)
+    spread = torch.zeros_like(out)
+    for s, n in enumerate(d["kv_len"].tolist()):
+        lo = max(0, n - N - window + 1) if window else 0
+        j = torch.arange(lo, max(n, 0), device=DEV)
+        if len(j) == 0:
+            continue
+        at = d["block_table"][s].long()[j // page]
+        k, v = (d[c][at, :, j % page].double().transpose(0, 1) for c in ("k_cache", "v_cache"))   # [Hkv, n, D]
+        q = d["q"][s].double().view(N, Hkv, Hq // Hkv, D)
+        pos = (n - N + torch.arange(N, device=DEV))[:, None]
+        see = (j <= pos) & (j > pos - window if window else j >= 0)                             # [N, n]
+        z = torch.einsum("ihgd,hnd->hgin", q, k) * scale
+        z = z.masked_fill(~see, -torch.inf)
+        e = torch.exp(z - z.amax(-1, keepdim=True).clamp(min=-1e300))
+        p = e / e.sum(-1, keepdim=True).clamp(min=1e-300)
+        for to, x in ((out, v), (spread, v.abs())):
+            to[s] = torch.einsum("hgin,hnd->ihgd", p, x).reshape(N, Hq, D)
+    return out, spread
+
+
+def limit(d, want, spread, scale=None):
+    """The tolerance of the attention's outputs (see test_gpu_block.py)."""
+    D = d["q"].shape[-1]
+    big = d["q"].double().norm(dim=-1).max() * torch.nan_to_num(d["k_cache"].float()).norm(dim=-1).max()
+    dz = (D + 4) * EPS * (D ** -0.5 if scale is None else scale) * big
+    return HALF * want.abs() + (HALF + 4 * dz + 2.0 ** -17) * spread
+
+
+def check64(d, window, got):
+    want, spread = attention64(d, window)
+    over = (got.double() - want).abs() - limit(d, want, spread)
+    assert (over <= 0).all(), float(over.max())
+    assert mm.moe_get_device_status() == (0, 0)
+
+
+# ------------------------------------------------ rows that fill a block in part --
+
+@pytest.mark.parametrize("c", [
+    # N, Hq, Hkv, D, page, window: rows to a key/value head, of them in the last block
+    (33, 10, 2, 64, 16, 0),        # 165, 37
+    (16, 5, 1, 64, 5, 0),          # 80
+    (24, 7, 1, 64, 64, 1000),      # 168, 40
+    (17, 8, 1, 128, 32, 0),        # 136, 8
+    (16, 10, 2, 128, 24, 700),     # 80
+    (20, 8, 1, 128, 7, 0),         # 160, 32
+    (33, 14, 2, 128, 128, 0),      # 231, 103 (every warp has rows)
+    (17, 16, 2, 256, 16, 0),       # 136, 8
+    (33, 6, 1, 256, 64, 500),      # 198, 70
+], ids=str)
+def test_attention_rows_that_fill_a_block_in_part(c):
+    """Softmax warps without rows beside those that have some, over segments of many
+    tiles: each tile's weights are complete before its product with the values."""
+    N, Hq, Hkv, D, page, window = c
+    lens = [600 + (s * 1709) % 3400 for s in range(64)]
+    st, _ = attention_case((64, N, Hq, Hkv, D, page, lens, window), 91)
+    d = to_dev(st)
+    ws = mm.alloc_attention_workspace(64, N, Hq, Hkv, D, DEV)
+    outs = [mm.block_attention(**d, window=window, workspace=ws) for _ in range(6)]
+    d = {k: torch.nan_to_num(v) if v.is_floating_point() else v for k, v in d.items()}
+    check64(d, window, outs[0])
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
