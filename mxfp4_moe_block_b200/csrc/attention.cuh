@@ -323,9 +323,9 @@ __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// One row's sum over the keys [k0, k1) of its sequence, for rows that do not see
-// all keys of a segment whose values are not all finite: in the product with V a
-// key that the row does not see weighs 0, and 0 x NaN or infinity would be NaN.
+// One row's sum over the keys [k0, k1) of its sequence, for rows in whose product
+// with V some key of a segment weighs 0 though not all values are finite: 0 x NaN
+// or infinity would be NaN.
 // A warp: lanes take a key each for the scores, then D/32 dims each for the sum.
 template <int D>
 __device__ __noinline__ void attn_row_alone(const AttnArgs &a, int s, int tok, int head, int k0,
@@ -976,8 +976,10 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           if (c + 1 < D / 32) softmax_sync<C::kSoftmax>();
         }
         if (!softmax_all<C::kSoftmax>(finite)) {
-          // values that are not finite: the rows that do not see all of the segment's
-          // keys are summed anew over those that they see
+          // values that are not finite: the rows in whose product some of the segment's
+          // keys weigh 0 are summed anew over the keys that they see.  Those are the rows
+          // that do not see all of them, and with lane groups every row (the other
+          // groups' keys weigh 0, and an infinity would come out as NaN).
           if (wg == 0 && kq == 0) ml[r] = make_float2(base, inv);
           softmax_sync<C::kSoftmax>();
           const int ka = max(w.q.lo, w.q.start + w.t0 * a.tile_keys);
@@ -985,7 +987,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           for (int rr = warp; rr < rows; rr += C::kSoftmax / 32) {
             const int at = w.rb * ATTN_ROWS + rr, i = at / group, p = w.q.n - a.N + i;
             const int k0 = max(ka, a.window > 0 ? p - a.window + 1 : 0), k1 = min(kb, p + 1);
-            if (k0 == ka && k1 == kb) continue;
+            if (KS == 1 && k0 == ka && k1 == kb) continue;
             attn_row_alone<D>(a, w.s, i, w.kvh * group + at - i * group, k0, k1, ml[rr].x, ml[rr].y,
                               whole ? item - (tid & 7) * 4 + row_at[rr] : nullptr,
                               reinterpret_cast<float *>(piece - (tid & 7) + (size_t)rr * (D / 4)));

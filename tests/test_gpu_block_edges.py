@@ -83,3 +83,56 @@ def test_attention_rows_that_fill_a_block_in_part(c):
     d = {k: torch.nan_to_num(v) if v.is_floating_point() else v for k, v in d.items()}
     check64(d, window, outs[0])
     assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+# --------------------------------------------------- values that are not finite --
+
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [
+    (1, 8, 1, 128), (8, 8, 2, 64), (12, 8, 2, 64), (16, 16, 2, 128), (33, 4, 1, 64),
+    (5, 6, 2, 256), (10, 8, 2, 256), (4, 32, 2, 128)], ids=str)
+def test_attention_infinite_values_come_out_as_such(N, Hq, Hkv, D, window):
+    """An infinite value is the result of every token that sees it, whatever the
+    number of rows; with one of each sign the result is NaN; a token that does not
+    see it is not touched."""
+    lens, page = [700, 90, 2000], 16
+    st, _ = attention_case((3, N, Hq, Hkv, D, page, lens, window), 92)
+    d = {k: torch.nan_to_num(v) if v.is_floating_point() else v for k, v in to_dev(st).items()}
+    inf = float("inf")
+    # (key, dims, value): two that all tokens see, one that the last alone sees
+    marks = lambda n: [(n - N - 3, 5, inf), (n - N - 40, 6, -inf), (n - N - 3, 4, inf), (n - N - 40, 4, -inf),
+                       (n - 1, 3, inf)]
+    clean = d["v_cache"].clone()
+    for s, n in enumerate(lens):
+        for key, dim, value in marks(n):
+            d["v_cache"][d["block_table"][s, key // page], :, key % page, dim::7] = value
+            clean[d["block_table"][s, key // page], :, key % page, dim::7] = 0
+    want, spread = attention64({**d, "v_cache": clean}, window)
+    lim = limit(d, want, spread)
+    for s in range(3):
+        want[s, :, :, 5::7], want[s, :, :, 6::7], want[s, :, :, 4::7] = inf, -inf, float("nan")
+        want[s, N - 1, :, 3::7] = inf
+    got = mm.block_attention(**d, window=window).double()
+    assert mm.moe_get_device_status() == (0, 0)
+    fine = want.isfinite()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()])
+    assert ((got - want).abs()[fine] <= lim[fine]).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(3, 8, 2, 128), (12, 8, 2, 64), (16, 16, 2, 128), (33, 4, 1, 64), (5, 6, 2, 256)])
+def test_attention_keys_that_are_not_finite_reach_no_other_token(N, Hq, Hkv, D, value):
+    """The last token's key: a score of +infinity or NaN makes the last token's result
+    NaN, one of -infinity weighs nothing; the other tokens are as without it."""
+    lens, page = [700, 90, 2000], 16
+    st, _ = attention_case((3, N, Hq, Hkv, D, page, lens, 0), 94)
+    d = {k: torch.nan_to_num(v) if v.is_floating_point() else v for k, v in to_dev(st).items()}
+    lim = limit(d, *attention64(d, 0))
+    for s, n in enumerate(lens):
+        d["k_cache"][d["block_table"][s, (n - 1) // page], :, (n - 1) % page, 0] = value
+    want, _ = attention64(d, 0)
+    got = mm.block_attention(**d).double()
+    assert mm.moe_get_device_status() == (0, 0)
+    assert torch.equal(got.isnan(), want.isnan()) and want[:, -1].isnan().any() and not want[:, :-1].isnan().any()
+    assert ((got - want).abs() <= lim)[~want.isnan()].all()
