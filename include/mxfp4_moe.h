@@ -429,7 +429,9 @@ int block_kv_append(const uint16_t *qkv, int S, int N, int Hq, int Hkv, int D, i
  *   0, or a negative position) gets zeros.  Cache rows at or past kv_len, and
  *   pages that no token of the block sees, are never used, whatever they or
  *   their page ids hold; a key or value that is not finite reaches the tokens
- *   that see it and no others.
+ *   that see it and no others, at a cost: where one is seen, tokens of its
+ *   sequence are summed anew key by key (17, 44 and 74 ns a key and query head
+ *   on one SM with D 64, 128 and 256).
  *   q, out      [S, N, Hq, D] bf16; out must not overlap the inputs
  *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16
  *   block_table [S, max_pages] int32; kv_len [S] int32

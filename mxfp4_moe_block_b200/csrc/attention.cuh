@@ -199,15 +199,24 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Bounded wait, inline: the softmax threads hold a tile of scores in
-// registers, which a call would have to spill.
-__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+// registers, which a call would have to spill.  The MMA warp and the producers
+// also wait while rows are summed anew (attn_row_alone), for as long as their
+// keys take: a beat counts that work, and the limit starts again when it has moved.
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          const volatile uint32_t *beat = nullptr) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
+  uint64_t t0 = global_ns();
+  uint32_t seen = beat ? *beat : 0;
   const uint64_t limit = *(volatile unsigned long long *)&g_wait_limit_ns;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_ns() - t0 >= limit) {
+      if (beat && *beat != seen) {
+        seen = *beat;
+        t0 = global_ns();
+        continue;
+      }
       raise_status(MOE_DEV_TIMEOUT);
       *abort = 1;
       return false;
@@ -327,10 +336,13 @@ __device__ __forceinline__ void softmax_sync() {
 // with V some key of a segment weighs 0 though not all values are finite: 0 x NaN
 // or infinity would be NaN.
 // A warp: lanes take a key each for the scores, then D/32 dims each for the sum.
+// Every ATTN_BEAT keys of its rows (`done` so far, returned) it counts `beat` up: a
+// segment may have more keys than fit the limit of the waits beside it (see attn_wait).
+constexpr int ATTN_BEAT = 32768;
 template <int D>
-__device__ __noinline__ void attn_row_alone(const AttnArgs &a, int s, int tok, int head, int k0,
+__device__ __noinline__ int attn_row_alone(const AttnArgs &a, int s, int tok, int head, int k0,
                                             int k1, float base, float f, uint16_t *out16,
-                                            float *out32) {
+                                            float *out32, int done, uint32_t *beat) {
   constexpr int W = D / 64;                              // words of two dims per lane
   const int lane = threadIdx.x & 31, kvh = head / (a.Hq / a.Hkv);
   const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (((size_t)s * a.N + tok) * a.Hq + head) * D);
@@ -338,6 +350,8 @@ __device__ __noinline__ void attn_row_alone(const AttnArgs &a, int s, int tok, i
 #pragma unroll
   for (int e = 0; e < 2 * W; ++e) o[e] = 0.f;
   for (int b = k0; b < k1; b += 32) {
+    done += 32;
+    if (lane == 0 && done % ATTN_BEAT == 0) atomicAdd(beat, 1u);
     const int key = b + lane;
     long long at = -1;                                   // this lane's row of the cache
     float p = 0.f;
@@ -380,6 +394,7 @@ __device__ __noinline__ void attn_row_alone(const AttnArgs &a, int s, int tok, i
     else
       reinterpret_cast<float2 *>(out32)[lane * W + e] = make_float2(o[2 * e], o[2 * e + 1]);
   }
+  return done;
 }
 
 template <int D, int KS>
@@ -410,6 +425,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
   int *const s_start = reinterpret_cast<int *>(drain + 2);                     // first sequence
   uint32_t *const issued = reinterpret_cast<uint32_t *>(drain + 4);            // [2] K, V tiles
   u64 *const s_base = reinterpret_cast<u64 *>(drain + 3);
+  uint32_t *const beat = reinterpret_cast<uint32_t *>(drain + 5);              // (attn_wait)
   u64 *const scan = reinterpret_cast<u64 *>(s_q);                              // before Q arrives
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -427,7 +443,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
     mbar_init(q_full, C::kSoftmax);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    issued[0] = issued[1] = 0;
+    issued[0] = issued[1] = *beat = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == MMA_WARP) {
@@ -555,7 +571,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           uint64_t *const bar = full + rg.slot;
           uint8_t *const to = s_ring + rg.slot * C::kSlot;
           const uint32_t dst = smem_u32(to);
-          ok = __all_sync(FULL, attn_wait(empty + rg.slot, rg.phase ^ 1, abort_flag));
+          ok = __all_sync(FULL, attn_wait(empty + rg.slot, rg.phase ^ 1, abort_flag, beat));
           if (!ok) break;
           // lane = page + boxes * column block of 64 dims (32 boxes at most)
           const int pg = lane % max(boxes, 1), c64 = lane / max(boxes, 1);
@@ -660,7 +676,7 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
       AttnRing<C::kSlots> kr(0), vr(2);
       bool ok = true;                                    // (lanes agree after a vote per tile)
       auto wait = [&](uint64_t *bar, uint32_t parity) {
-        ok = ok && attn_wait(bar, parity, abort_flag);
+        ok = ok && attn_wait(bar, parity, abort_flag, beat);
       };
       // S[tt & 1] = Q K^T, its K tile waited for
       auto scores = [&](uint32_t tt) {
@@ -984,13 +1000,15 @@ attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ C
           softmax_sync<C::kSoftmax>();
           const int ka = max(w.q.lo, w.q.start + w.t0 * a.tile_keys);
           const int kb = (int)min((long long)w.q.n, w.q.start + (long long)w.t1 * a.tile_keys);
+          int done = 0;
           for (int rr = warp; rr < rows; rr += C::kSoftmax / 32) {
             const int at = w.rb * ATTN_ROWS + rr, i = at / group, p = w.q.n - a.N + i;
             const int k0 = max(ka, a.window > 0 ? p - a.window + 1 : 0), k1 = min(kb, p + 1);
             if (KS == 1 && k0 == ka && k1 == kb) continue;
-            attn_row_alone<D>(a, w.s, i, w.kvh * group + at - i * group, k0, k1, ml[rr].x, ml[rr].y,
-                              whole ? item - (tid & 7) * 4 + row_at[rr] : nullptr,
-                              reinterpret_cast<float *>(piece - (tid & 7) + (size_t)rr * (D / 4)));
+            done = attn_row_alone<D>(
+                a, w.s, i, w.kvh * group + at - i * group, k0, k1, ml[rr].x, ml[rr].y,
+                whole ? item - (tid & 7) * 4 + row_at[rr] : nullptr,
+                reinterpret_cast<float *>(piece - (tid & 7) + (size_t)rr * (D / 4)), done, beat);
           }
           softmax_sync<C::kSoftmax>();
         }

@@ -136,3 +136,27 @@ def test_attention_keys_that_are_not_finite_reach_no_other_token(N, Hq, Hkv, D, 
     assert mm.moe_get_device_status() == (0, 0)
     assert torch.equal(got.isnan(), want.isnan()) and want[:, -1].isnan().any() and not want[:, :-1].isnan().any()
     assert ((got - want).abs() <= lim)[~want.isnan()].all()
+
+
+@pytest.mark.parametrize("N,Hq,D", [(16, 64, 128), (16, 64, 64), (8, 64, 256)], ids=str)
+def test_attention_summing_anew_outlasts_the_wait_limit(N, Hq, D):
+    """A value that is not finite in a long cache: its sequence's other rows are summed
+    anew key by key, while the waits for the next sequence's tiles run on.  They are not
+    cut short by a limit that the summing as a whole passes.  (Of one sequence and head
+    it takes 36 to 92 ms, and up to 10 ms to a beat, 32768 keys of a warp.)"""
+    S, Hkv, page, n = 40, 8, 64, 16384
+    st, _ = attention_case((1, N, Hq, Hkv, D, page, [n], 0), 93)
+    d = {k: torch.nan_to_num(v) if v.is_floating_point() else v for k, v in to_dev(st).items()}
+    d["q"], d["block_table"], d["kv_len"] = (t.repeat_interleave(S, 0) for t in (d["q"], d["block_table"], d["kv_len"]))
+    one = {**d, "q": d["q"][:1], "block_table": d["block_table"][:1], "kv_len": d["kv_len"][:1]}
+    want, spread = attention64(one, 0)
+    lim = limit(d, want, spread)
+    d["v_cache"][d["block_table"][0, (n - 1) // page], :, (n - 1) % page] = float("nan")
+    try:
+        mm.moe_set_wait_limit_ns(15_000_000)
+        out = mm.block_attention(**d).double()
+        assert mm.moe_get_device_status() == (0, 0)
+    finally:
+        mm.moe_set_wait_limit_ns(0)
+    assert out[:, -1].isnan().all()
+    assert ((out[:, :-1] - want[:, :-1]).abs() <= lim[:, :-1]).all()
