@@ -92,13 +92,12 @@ kv_append_kernel(const AppendArgs a) {
 
   // this lane's cosines and sines: dims 8l..8l+7 turn with frequency
   // (dim mod rot/2), or with dim/2 where neighbours are pairs.  Pairs of halves:
-  // x c + partner s, the sine's sign the half's; lanes past rot: c = 1, s = 0.
+  // x c + partner s, the sine's sign the half's.  Lanes past rot keep their dims (by
+  // c = 1, s = 0 an infinity would become NaN).
   const int half = a.rot / 2;
   const bool turns = 8 * l < a.rot && pos < a.max_pos;
   const bool upper = 8 * l >= half;                // the pair's second element (halves)
-  float c[8], sn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = 1.f, sn[e] = 0.f;
+  float c[8] = {}, sn[8] = {};
   if (turns) {
     const float *row = a.cos_sin + (size_t)pos * a.rot;
     if (a.interleaved) {
@@ -151,15 +150,15 @@ kv_append_kernel(const AppendArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float p = x[2 * e], q = x[2 * e + 1];
-            x[2 * e] = p * c[e] - q * sn[e];
-            x[2 * e + 1] = p * sn[e] + q * c[e];
+            x[2 * e] = turns ? p * c[e] - q * sn[e] : p;
+            x[2 * e + 1] = turns ? p * sn[e] + q * c[e] : q;
           }
         } else {
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(FULL, x[e], partner, LANES);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e], sn[e], x[e] * c[e]);
+          for (int e = 0; e < 8; ++e) x[e] = turns ? fmaf(y[e], sn[e], x[e] * c[e]) : x[e];
         }
       }
       if (!is_v)

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import mxfp4_moe_block_b200 as mm
-from test_gpu_block import DEV, EPS, HALF, attention_case, clean_status, to_dev  # noqa: F401
+from test_gpu_block import DEV, EPS, HALF, attention_case, clean_status, cos_sin, to_dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +160,27 @@ def test_attention_summing_anew_outlasts_the_wait_limit(N, Hq, D):
         mm.moe_set_wait_limit_ns(0)
     assert out[:, -1].isnan().all()
     assert ((out[:, :-1] - want[:, :-1]).abs() <= lim[:, :-1]).all()
+
+
+# -------------------------------------------------- dims that are not rotated --
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 16), (64, 48), (128, 64), (256, 32), (256, 240)])
+def test_append_infinities_in_dims_that_are_not_rotated(D, rot, interleaved):
+    """Without norms the dims past `rot` pass through, whatever they hold."""
+    S, N, Hq, Hkv, page, n = 2, 3, 6, 2, 16, 40
+    g = torch.Generator().manual_seed(D + rot)
+    qkv = torch.randn((S, N, Hq + 2 * Hkv, D), generator=g).to(torch.bfloat16)
+    qkv[..., rot + 1::3] = float("inf")
+    qkv[..., rot + 5::9] = -float("inf")
+    qkv[..., rot + 6::11] = float("nan")
+    cs = cos_sin(n, rot).to(DEV)
+    table = torch.arange(S * 3, dtype=torch.int32, device=DEV).view(S, 3)
+    kc, vc = (torch.zeros((S * 3, Hkv, page, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q = mm.block_kv_append(qkv.to(DEV), torch.full((S,), n, dtype=torch.int32, device=DEV), table, kc, vc,
+                           cs, norm=False, interleaved=interleaved).cpu()
+    at = torch.arange(n - N, n)
+    k = kc.cpu()[table.cpu().long()[:, at // page], :, at % page]                        # [S, N, Hkv, D]
+    for got, want in ((q, qkv[:, :, :Hq]), (k, qkv[:, :, Hq:Hq + Hkv])):
+        torch.testing.assert_close(got[..., rot:], want[..., rot:], rtol=0, atol=0, equal_nan=True)
+    assert q[..., :rot].isfinite().all() and k[..., :rot].isfinite().all()
