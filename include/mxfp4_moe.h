@@ -457,7 +457,8 @@ int block_attention(const uint16_t *q, int S, int N, int Hq, int Hkv, int D,
  *   block_accept_rejection reads, and the drafter's tokens.  (The pages verify
  *   by rejection sampling, [P3] "数据流概览", and do not say how the
  *   distributions are formed.)  For a row with logits l:
- *     w_v = exp((l_v - max l) / temperature), W_v = floor(w_v * 2^40), double;
+ *     w_v = exp((l_v - max l) / temperature), W_v = floor(w_v * 2^40) (w_v in
+ *     double: within 2^-12 of a whole number w_v * 2^40 may fall to either side);
  *     tokens ranked by logit, ties to the lowest index; kept is the longest
  *     prefix of that ranking which every filter allows:
  *       top-k  the first k;

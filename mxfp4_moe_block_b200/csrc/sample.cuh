@@ -26,7 +26,7 @@
 //
 // Bounds.  The bytes: a row in and, where wanted, its probabilities out.  The
 // exponentials: an SM does 64 double operations a cycle and a weight with its mass
-// takes 12 (and two conversions, 16 a cycle), ~5 weights per cycle and SM, against
+// takes 10 (and two conversions, 16 a cycle), ~6 weights per cycle and SM, against
 // ~6 logits per cycle that HBM delivers to an SM.  So a kept token's weight is
 // computed once (top-p over a whole row: every weight, and the kept ones again);
 // where few are kept they wait in a queue until a warp has 32 of them; the float of
@@ -35,8 +35,8 @@
 // between them, 8 us for a row of 32000 without filters, 19 with top-p, hidden by
 // other rows only as far as two CTAs fit an SM (issue slots 58 % busy, DRAM 16 %).
 // Measured, with probabilities: 128 rows of 152064, mixed filters, 122 us (24 us at
-// HBM's rate); 1024 rows of 32000, temperature 107 us (40 us), top-k 50 135 us,
-// top-p 0.9 266 us; one row of 32000 under every filter, token only, 13 us.
+// HBM's rate); 1024 rows of 32000, temperature 109 us (40 us), top-k 50 133 us,
+// top-p 0.9 261 us; one row of 32000 under every filter, token only, 13 us.
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -80,15 +80,24 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 
 // 2^40 w = 2^(d c + 40), d = x - top <= 0, c = log2(e) / temperature, for
 // d c > -1000 (the caller takes 0 for less).  The exponent's nearest integer
-// comes from float (it need not be exact: the remainder f is), 2^f on
-// [-1/2, 1/2] is 1 + f p(f), p of degree 7 fitted to the least relative error
-// at Chebyshev nodes: 2^-40, the masses' own step.  11 double operations and
-// two conversions.
+// comes from float (it need not be exact: the remainder f is), counted in 16ths.  Of
+// 2^(n + j/16 + f) the middle factor is looked up (16 doubles, a shared memory bank
+// pair each: no conflicts) and 2^f on [-1/32, 1/32] is 1 + f p(f), p of degree 5
+// fitted to the least relative error at Chebyshev nodes: 2^-55.8.  With the rounding
+// of what it takes 2^40 w comes within 2^-12 of its value, so a mass can differ from the
+// definition's floor only where that lies as near to a whole number (5 of 10^5 masses
+// above 2^39).  9 double operations and two conversions.
+__constant__ double kSampleSteps[16] = {
+    1.0, 1.0442737824274138, 1.0905077326652577, 1.1387886347566916,
+    1.189207115002721, 1.241857812073484, 1.2968395546510096, 1.3542555469368927,
+    1.4142135623730951, 1.4768261459394993, 1.5422108254079407, 1.6104903319492543,
+    1.681792830507429, 1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
 struct SampleScale {
   double top, c, halving;         // halving: logits to a factor of two
   float ftop, fc, lowest;         // logits below `lowest` (d c < -1000) weigh 0
-  __device__ __forceinline__ SampleScale(float t, double temperature)
-      : top((double)t), c(1.4426950408889634 / temperature),
+  const double *steps;            // 2^(j/16), in shared memory
+  __device__ __forceinline__ SampleScale(float t, double temperature, const double *steps)
+      : steps(steps), top((double)t), c(1.4426950408889634 / temperature),
         halving(temperature * 0.6931471805599453), ftop(t), fc((float)c) {
     const double least = fma(-1000.0, halving, top);
     lowest = fmaxf((float)least, -FLT_MAX);
@@ -96,19 +105,19 @@ struct SampleScale {
   }
   __device__ __forceinline__ bool positive(float x) const { return x >= lowest; }   // NaN: no
   __device__ __forceinline__ double weight(float x) const {
-    const float magic = 12582912.f + 40.f;                          // 1.5 2^23, and the 2^40
+    const float magic = 786432.f + 40.f;                            // 1.5 2^19, and the 2^40
     const float shifted = fmaf(x - ftop, fc, magic);
+    const int b = __float_as_int(shifted);
     const double f = fma((double)x - top, c, -(double)(shifted - magic));
-    double p = 1.318882399508972e-06;
-    p = fma(p, f, 1.5309693155944608e-05);
-    p = fma(p, f, 0.00015403775196491106);
-    p = fma(p, f, 0.001333345225539645);
-    p = fma(p, f, 0.00961812869532959);
-    p = fma(p, f, 0.05550410939101241);
-    p = fma(p, f, 0.2402265069773642);
-    p = fma(p, f, 0.6931471805465889);
-    p = fma(p, f, 1.0);
-    return __hiloint2double(__double2hiint(p) + (__float_as_int(shifted) << 20), __double2loint(p));
+    const double t = steps[b & 15];
+    double p = 0.0001540372522169807;
+    p = fma(p, f, 0.001333378300903704);
+    p = fma(p, f, 0.00961812910691042);
+    p = fma(p, f, 0.05550410865653406);
+    p = fma(p, f, 0.24022650695910075);
+    p = fma(p, f, 0.6931471805599457);
+    p = fma(t * f, p, t);
+    return __hiloint2double(__double2hiint(p) + ((b & ~15) << 16), __double2loint(p));
   }
 };
 // floor(2^40 w), 2^-960 < 2^40 w <= 2^40: added to 2^52 the integer part is the
@@ -144,6 +153,7 @@ struct SampleRow {
     int list_n;                // tokens in this CTA's list
     int above_n;               // and of its slice above the threshold's bucket
     int pos;
+    double steps[16];          // (SampleScale)
   };
 };
 
@@ -250,6 +260,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
         val[4 * j + i] = v + i >= c0 && v + i < c1 ? x[v + i] : __int_as_float(0x7fffffff);
     }
   }
+  if (tid < 16) sh.steps[tid] = kSampleSteps[tid];
   const double T = a.temperature ? (double)__ldg(a.temperature + s) : 1.0;
   const int k = a.top_k ? __ldg(a.top_k + s) : 0;
   const double p = a.top_p ? (double)__ldg(a.top_p + s) : 1.0;
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     return;                                       // (no remote access after the exchange)
   }
   // (limits that keep the scale, its reciprocal and its products finite in float)
-  const SampleScale z(top, fmin(fmax(T, 1e-36), 1e30));
+  const SampleScale z(top, fmin(fmax(T, 1e-36), 1e30), sh.steps);
   auto mass_at = [&](float l) -> u64 { return z.positive(l) ? sample_mass(z.weight(l)) : 0; };
 
   // ---- the threshold: kept are logits above `at`, and at it the tokens <= last ----

@@ -6,6 +6,7 @@ The attention is compared with `attention64`, the definition in float64 on the
 device (the oracle's loops are too slow for these sizes), under the tolerance
 that test_gpu_block.py derives.
 """
+import numpy as np
 import pytest
 import torch
 
@@ -184,3 +185,64 @@ def test_append_infinities_in_dims_that_are_not_rotated(D, rot, interleaved):
     for got, want in ((q, qkv[:, :, :Hq]), (k, qkv[:, :, Hq:Hq + Hkv])):
         torch.testing.assert_close(got[..., rot:], want[..., rot:], rtol=0, atol=0, equal_nan=True)
     assert q[..., :rot].isfinite().all() and k[..., :rot].isfinite().all()
+
+
+# ------------------------------------------------------ masses at a filter's border --
+
+def border_logits(temperature, seed):
+    """Logits l below a largest one of 0 whose mass W = floor(2^40 exp(l / T)) lies at a
+    multiple of 2^16 or one below it, so that a float min_p tells the two apart; those
+    with 2^40 exp(l / T) within 0.02 of a whole number are left out (numpy's exponential
+    is good to 2^-11 there).  Returns (l, W)."""
+    l = -np.random.default_rng(seed).uniform(1e-3, 0.69 * temperature, 1 << 23).astype(np.float32)
+    y = np.exp(l.astype(np.float64) / temperature) * 2.0 ** 40
+    W = np.floor(y)
+    frac, step = y - W, W % 65536
+    pick = (frac > 0.02) & (frac < 0.98) & ((step == 0) | (step == 65535))
+    return l[pick], W[pick].astype(np.int64)
+
+
+def kept_second(l, **f):
+    """Whether the token of logit l is kept beside one of logit 0."""
+    z = torch.zeros((len(l), 1, 5))
+    z[:, 0, 3] = torch.from_numpy(l)
+    z[:, 0, [0, 2, 4]] = -40.0
+    _, probs = mm.block_sample(z.to(DEV), **{k: v.to(DEV) for k, v in f.items()}, with_probs=True)
+    return (probs[:, 0, 3] > 0).cpu().numpy()
+
+
+@pytest.mark.parametrize("T", [1.0, 0.75, 3.0])
+@pytest.mark.parametrize("beside", ["alone", "top_k", "top_p"])
+def test_sample_masses_at_the_min_p_border(T, beside):
+    l, W = border_logits(T, int(T * 4))
+    assert len(l) > 100 and (W % 65536 == 0).any() and (W % 65536 != 0).any()
+    low = (W + 65535) // 65536                               # min_p 2^24
+    f = dict(temperature=torch.full((len(l),), T), min_p=torch.from_numpy(low * 2.0 ** -24).float())
+    if beside == "top_k":
+        f["top_k"] = torch.full((len(l),), 3, dtype=torch.int32)
+    elif beside == "top_p":
+        f["top_p"] = torch.full((len(l),), 1 - 2.0 ** -24)
+    assert np.array_equal(kept_second(l, **f), W >= low * 65536)
+
+
+def test_sample_masses_at_the_top_p_border():
+    """Two tokens and a float p at which one unit of the second's mass decides whether
+    the first alone reaches p of the sum."""
+    l = -np.random.default_rng(5).uniform(1e-3, 0.69, 1 << 24).astype(np.float32)
+    w = np.exp(l.astype(np.float64))
+    p = np.round(2.0 ** 24 / (1 + w)) * 2.0 ** -24
+    near = abs(p * (1 + w) - 1) * 2.0 ** 40 < 2
+    l, w, p = l[near], w[near], p[near]
+    y = w * 2.0 ** 40
+    W = np.floor(y)
+    stays = lambda m: np.ceil(p * (2.0 ** 40 + m)) > 2.0 ** 40
+    pick = (y - W > 0.02) & (y - W < 0.98) & (stays(W - 1) != stays(W + 1))
+    assert pick.sum() > 100
+    l, p, want = l[pick], p[pick], stays(W)[pick]
+    assert want.any() and not want.all()
+    for V, f in ((2, {}), (5, dict(top_k=torch.full((len(l),), 2, dtype=torch.int32)))):
+        z = torch.full((len(l), 1, V), -60.0)
+        z[:, 0, 0], z[:, 0, 1] = 0.0, torch.from_numpy(l)
+        f = {k: v.to(DEV) for k, v in dict(f, top_p=torch.from_numpy(p).float()).items()}
+        _, probs = mm.block_sample(z.to(DEV), **f, with_probs=True)
+        assert np.array_equal((probs[:, 0, 1] > 0).cpu().numpy(), want)
