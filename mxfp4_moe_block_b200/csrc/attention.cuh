@@ -199,29 +199,45 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Bounded wait, inline: the softmax threads hold a tile of scores in
-// registers, which a call would have to spill.  The MMA warp and the producers
-// also wait while rows are summed anew (attn_row_alone), for as long as their
-// keys take: a beat counts that work, and the limit starts again when it has moved.
-__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                          const volatile uint32_t *beat = nullptr) {
+// registers, which a call would have to spill.
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = global_ns();
-  uint32_t seen = beat ? *beat : 0;
+  const uint64_t t0 = global_ns();
   const uint64_t limit = *(volatile unsigned long long *)&g_wait_limit_ns;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (global_ns() - t0 >= limit) {
-      if (beat && *beat != seen) {
-        seen = *beat;
-        t0 = global_ns();
-        continue;
-      }
       raise_status(MOE_DEV_TIMEOUT);
       *abort = 1;
       return false;
     }
   }
+}
+// The same for the MMA warp and the producers, which also wait while rows are
+// summed anew (attn_row_alone), for as long as their keys take: a beat counts that
+// work, and the limit starts again when it has moved.
+__device__ __noinline__ bool attn_wait_on(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          const volatile uint32_t *beat) {
+  uint64_t t0 = global_ns();
+  uint32_t seen = *beat;
+  const uint64_t limit = *(volatile unsigned long long *)&g_wait_limit_ns;
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 >= limit) {
+      if (*beat == seen) break;
+      seen = *beat;
+      t0 = global_ns();
+    }
+  }
+  raise_status(MOE_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                          const volatile uint32_t *beat) {
+  return mbar_try_wait(bar, parity) || attn_wait_on(bar, parity, abort, beat);
 }
 
 // 16-byte unit u of row r in a tile of `rows` rows: blocks of 64 dims, swizzled
