@@ -6,12 +6,15 @@ The attention is compared with `attention64`, the definition in float64 on the
 device (the oracle's loops are too slow for these sizes), under the tolerance
 that test_gpu_block.py derives.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import mxfp4_moe_block_b200 as mm
-from test_gpu_block import DEV, EPS, HALF, attention_case, clean_status, cos_sin, to_dev  # noqa: F401
+from test_gpu_block import (DEV, EPS, HALF, attention_case, check_step, clean_status, cos_sin,  # noqa: F401
+                            step_state, to_dev, verify_step)
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +249,32 @@ def test_sample_masses_at_the_top_p_border():
         f = {k: v.to(DEV) for k, v in dict(f, top_p=torch.from_numpy(p).float()).items()}
         _, probs = mm.block_sample(z.to(DEV), **f, with_probs=True)
         assert np.array_equal((probs[:, 0, 1] > 0).cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ host threads --
+
+def test_verify_steps_of_several_host_threads():
+    """Four threads, a stream and a workspace each, all three calls."""
+    steps = [step_state(500 + i) for i in range(4)]
+    before = [{k: st[k].clone() for k in ("k", "v")} for st, _ in steps]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    verify_step(*steps[i])
+            stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for (st, out), b in zip(steps, before):
+        check_step(st, b, out)
