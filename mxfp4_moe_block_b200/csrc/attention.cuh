@@ -9,7 +9,10 @@
 // tensor memory.  At these row counts the cache's bytes bound the call (2 flops
 // per row and byte against ~250 flops per byte of the machine), so a padded
 // 128-row MMA costs nothing: a 64 KB tile (128 keys, D = 128) takes the tensor
-// pipe ~1000 cycles and an SM's share of HBM ~2700.
+// pipe ~1000 cycles and an SM's share of HBM ~2700.  More rows than 128 are several
+// row blocks, each of which reads the cache again (16 sequences of up to 30000 keys,
+// 64/8 heads of 128: 16 tokens, 128 rows 194 us; 17 tokens, 136 rows 336 us; 33
+// tokens, 264 rows 507 us).
 //
 // Softmax in one pass: every row keeps a maximum m and a sum l in float; O is
 // rescaled only when a tile's maximum exceeds m by 8 (in powers of two), so
@@ -31,7 +34,10 @@
 // and the V tiles of a shared ring in the 128-byte swizzle: by TMA page by page
 // where pages are multiples of 8 rows, or row by row through cp.async, where rows
 // outside the sequence or on a bad page are zero-filled and masked by a bit per
-// key.  (By rows alone: 16 sequences of up to 30000 keys 246 us, by TMA 156.)  The
+// key.  (By rows alone: 14 sequences of up to 30000 keys 246 us, by TMA 156; 16 sequences: pages of
+// 30 and 100 rows 281 and 273 us, of 16 to 256 that go by TMA 172 to 181, of 8 226.)
+// Where pages do not fill a tile (24, 40, 48 ..) the tile is the whole pages that fit,
+// and every score of it is tested for its key (pages of 24 179 us, of 32 174).  The
 // ring's order is that of use, K0 K1 V0 K2 V1 .., each tile scored two ahead of
 // its product with V.  For D = 64 a tile's bytes arrive in half the time, but its
 // weights take as long: two warpgroups take every other tile, each with an O of
@@ -41,12 +47,12 @@
 // to 32 rows (64) the queries stand in the 128 MMA rows four (two) times, lane
 // group g weighs the g-th quarter (half) of each tile's keys, its other weights
 // stay zero, and the groups' O, m and l are joined at the segment's end.  (64
-// sequences, 16 heads of 64, window: 37 us, without groups 51, with two 41; a
+// sequences, 16 heads of 64, window: 36 us, without groups 51, with two 41; a
 // sequence of 131000 keys, 8 rows to a head: 58 us, without 61.)
 //
-// Measured (floor: the visible cache once at a plain copy's rate): 16 sequences of
+// Measured (floor: the visible cache once at a plain copy's rate): 14 sequences of
 // up to 30000 keys, 64/8 heads of 128, 8 tokens 156 us (132); 64 of up to 9000,
-// 32/4 heads, 16 tokens 142 us (98); one of 131000, 32/4 heads, one token 58 us
+// 32/4 heads, 16 tokens 145 us (98); one of 131000, 32/4 heads, one token 58 us
 // (41); one of 777 keys 14 us (0.5).  What is left: the start of a call (barriers,
 // tensor memory, the pieces' places, the first tiles) 4-5 us, the join 4-6 us, the
 // output of an item 1.3 us, in which its CTA's loads run on into the ring only.

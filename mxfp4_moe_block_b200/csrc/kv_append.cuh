@@ -18,8 +18,10 @@
 // eight CTAs of 128 threads and 64 registers share an SM (the largest case below:
 // 37.4 us, with four of 256 threads 39.0, with three 43).  Measured: one token of 80
 // heads 2.4 us, 128 tokens of 56 heads 3.4 us (the launch), 4224 tokens of 80 heads
-// of 128 37 us: 175 MB at 4.7 TB/s, 0.72 of a plain copy's rate (the norms' shuffles
-// and the rotation fill the issue slots beside the loads).
+// of 128 37 us: 175 MB at 4.7 TB/s, 0.72 of a plain copy's rate (the shuffles, four a
+// head for the norm and eight for the rotation of halves, fill the issue slots beside
+// the loads; the eight are this layout's: a lane that held both units of a pair would
+// need none).
 #pragma once
 #include "common.cuh"
 

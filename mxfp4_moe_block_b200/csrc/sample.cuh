@@ -33,7 +33,9 @@
 // a weight stays in shared memory for the probabilities.  And the row's steps one
 // after another: five to nine barriers of the cluster and the first CTA's search
 // between them, 8 us for a row of 32000 without filters, 19 with top-p, hidden by
-// other rows only as far as two CTAs fit an SM (issue slots 58 % busy, DRAM 16 %).
+// other rows only as far as two CTAs fit an SM (issue slots 58 % busy, DRAM 16 %).  Two
+// it is by registers (64 of 512 threads); the shared memory of a slice of 16000 tokens
+// without filters would do for three.
 // Measured, with probabilities: 128 rows of 152064, mixed filters, 122 us (24 us at
 // HBM's rate); 1024 rows of 32000, temperature 109 us (40 us), top-k 50 133 us,
 // top-p 0.9 261 us; one row of 32000 under every filter, token only, 13 us.
@@ -353,8 +355,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
   // list's place) until there is one for every lane.  `zero`: the others become 0.
   const int wu = (units + SAMPLE_WARPS - 1) / SAMPLE_WARPS;         // units of a warp
   // top-p keeps a third of the slice or more: then each weight where it stands, else
-  // the queue (1024 rows of 32000, top-p 0.9: queue 266 us, in place 274; 0.99: 289
-  // and 276; top-p 0.7 252 and 269)
+  // the queue (1024 rows of 32000, top-p 0.9: queue 261 us, in place 272; 0.99: 285
+  // and 274; top-p 0.7 246 and 266)
   bool many = false;
   float least = -INFINITY;                       // no token below this logit is kept
   auto for_queued = [&](auto f, bool zero = false) {
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
     };
 
     // ---- a small top-k: the first CTA settles the row (1024 rows of 32000, top-k 50:
-    // 135 us, by the histograms below 173; with top-p 0.9 beside it 144 and 257) ----
+    // 133 us, by the histograms below 168; with top-p 0.9 beside it 142 and 253) ----
     // Every CTA lists its tokens down to the k-th largest of its threads' own maxima:
     // the k first-ranked of the row are among them, and few more than k of each CTA.
     SampleRow::Found f{};
@@ -1017,8 +1019,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleA
 
 // CTAs of a row: slices of at most 18432 tokens (72 KB, two CTAs per SM) and,
 // for few rows, enough CTAs for the machine with 2048 tokens each at least.  (1024
-// rows of 32000: two CTAs 110 us, one 129, four 156, the steps between barriers
-// being paid by each; a single row of 32000: eight CTAs 14.0 us, two 15.0.)
+// rows of 32000 at a temperature: two CTAs 109 us, one 118, four 150, the steps between
+// barriers being paid by each; a single row of 32000, all filters: eight CTAs 11.4 us,
+// two 11.9.)
 inline int sample_cluster(int rows, int V, int sms) {
   int c = 1;
   while (c < SAMPLE_MAX_CLUSTER &&
