@@ -34,25 +34,26 @@
 // and the V tiles of a shared ring in the 128-byte swizzle: by TMA page by page
 // where pages are multiples of 8 rows, or row by row through cp.async, where rows
 // outside the sequence or on a bad page are zero-filled and masked by a bit per
-// key.  (By rows alone: 14 sequences of up to 30000 keys 246 us, by TMA 156; 16 sequences: pages of
-// 30 and 100 rows 281 and 273 us, of 16 to 256 that go by TMA 172 to 181, of 8 226.)
+// key.  (By rows alone: 14 sequences of up to 30000 keys 241 us, by TMA 158.  With 16
+// sequences pages of 16 to 256 rows take 172 to 181 us, of 8 226, of 30 and 100, by
+// rows, 281 and 273.)
 // Where pages do not fill a tile (24, 40, 48 ..) the tile is the whole pages that fit,
 // and every score of it is tested for its key (pages of 24 179 us, of 32 174).  The
 // ring's order is that of use, K0 K1 V0 K2 V1 .., each tile scored two ahead of
 // its product with V.  For D = 64 a tile's bytes arrive in half the time, but its
 // weights take as long: two warpgroups take every other tile, each with an O of
-// its own (64 sequences of 5000 keys, 16 heads, 8 tokens: 256 us, with one 281).
+// its own (64 sequences of 5000 keys, 16 heads, 8 tokens: 278 us, with one 289).
 //
 // Few rows would leave most lanes, and so most softmax warps, without work: up
 // to 32 rows (64) the queries stand in the 128 MMA rows four (two) times, lane
 // group g weighs the g-th quarter (half) of each tile's keys, its other weights
 // stay zero, and the groups' O, m and l are joined at the segment's end.  (64
 // sequences, 16 heads of 64, window: 36 us, without groups 51, with two 41; a
-// sequence of 131000 keys, 8 rows to a head: 58 us, without 61.)
+// sequence of 131000 keys, 8 rows to a head: 58 us, without 62.)
 //
 // Measured (floor: the visible cache once at a plain copy's rate): 14 sequences of
-// up to 30000 keys, 64/8 heads of 128, 8 tokens 156 us (132); 64 of up to 9000,
-// 32/4 heads, 16 tokens 145 us (98); one of 131000, 32/4 heads, one token 58 us
+// up to 30000 keys, 64/8 heads of 128, 8 tokens 155-158 us (132); 64 of up to 9000,
+// 32/4 heads, 16 tokens 142-145 us (98); one of 131000, 32/4 heads, one token 58 us
 // (41); one of 777 keys 14 us (0.5).  What is left: the start of a call (barriers,
 // tensor memory, the pieces' places, the first tiles) 4-5 us, the join 4-6 us, the
 // output of an item 1.3 us, in which its CTA's loads run on into the ring only.
